@@ -58,11 +58,12 @@ typedef enum pa_status {
   PA_ERR_SEQ_SWAPPED = 7     /* sequence is swapped out (or, for swap-in, is not) */
 } pa_status;
 
-/* PA_FP8_E4M3 is a cache element type only: pa_reshape_and_cache_fp8 writes it,
- * pa_paged_decode_fp8 reads it, pa_copy_blocks and pa_swap_blocks move it (one
- * byte per element). Queries, outputs and the 16-bit inputs of the cache write
- * are PA_F16 or PA_BF16. */
-typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
+/* PA_FP8_E4M3 and PA_INT4 are cache element types only: pa_reshape_and_cache_fp8
+ * / _int4 write them, pa_paged_decode_fp8 / _int4 read them, pa_copy_blocks and
+ * pa_swap_blocks move them (one byte per element; head_dim/2 + 4 bytes per token
+ * and KV head). Queries, outputs and the 16-bit inputs of the cache writes are
+ * PA_F16 or PA_BF16. */
+typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } pa_dtype;
 
 /* Bits OR-ed into *dev_error by device calls. */
 #define PA_DEVERR_SLOT_RANGE 1    /* slot >= num_blocks * block_size: token not written */
@@ -75,6 +76,8 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
                                      range, a member claimed twice): that group's members
                                      were decoded without the shared prefix; outputs stay
                                      correct */
+#define PA_DEVERR_POSITION 32     /* a token's position outside [0, num_positions): the token
+                                     was neither rotated nor written */
 
 /* Message for the last failed call on this thread ("" if none). */
 const char* pa_last_error(void);
@@ -143,7 +146,8 @@ int pa_reshape_and_cache(const void* key, const void* value, int64_t key_token_s
  *           src of the same call (so the copies are independent). Violations
  *           return PA_ERR_INVALID_ARG and launch nothing.
  * The pairs travel in the kernel's parameter block: no device buffer is needed.
- * num_pairs == 0 is a no-op. dtype PA_FP8_E4M3 copies 8-bit caches.
+ * num_pairs == 0 is a no-op. dtype PA_FP8_E4M3 copies 8-bit caches, PA_INT4
+ * 4-bit ones.
  * ------------------------------------------------------------------------- */
 int pa_copy_blocks(void* k_cache, void* v_cache, const int64_t* pairs, int num_pairs,
                    int num_kv_heads, int head_dim, int block_size, int num_blocks, int dtype,
@@ -210,6 +214,134 @@ int pa_paged_decode_fp8(void* out, const void* q, const void* k_cache, const voi
                         int block_size, int num_blocks, float scale, float k_scale,
                         float v_scale, int partition_tokens, void* workspace,
                         size_t workspace_bytes, int* dev_error, int dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit KV cache: pa_reshape_and_cache_int4, pa_paged_decode_int4 and
+ * pa_read_slots_int4.
+ *
+ * The next step of KV-cache quantization ("PagedAttention: The vLLM Paper",
+ * "Impact and Follow-Ups" and "Limitations"); the pages fix no format. Format
+ * taken: every row (one token, one KV head, of K or of V) holds 4-bit codes and
+ * two halves of its own, scale and mid; a code n stands for
+ *   mid + (n - 7.5) * scale.
+ * Caches are byte arrays [num_blocks][Hkv][16][head_dim/2 + 4]; within a
+ * (block, KV head) tile the 16 rows' codes come first (8 * head_dim bytes),
+ * then 16 pairs (scale, mid):
+ *   k_cache  row t's codes are the head_dim/2 bytes at t * head_dim/2, dimension
+ *            2i in the low nibble of byte i and 2i + 1 in the high one;
+ *   v_cache  with W = head_dim/32 and p = t / 2, dimension x of row t is nibble
+ *            x % 2 of byte
+ *              ((p/4 * 32 + x/(4*W) * 4 + p%4) * W + x/4 % W) * 4 + t%2 * 2 + x%4 / 2
+ *            (whole-number divisions): the order in which the decode's matrix
+ *            instructions take the codes.
+ * Copy and swap these caches with dtype PA_INT4. The cascade takes 16- and 8-bit
+ * caches only.
+ *
+ * pa_reshape_and_cache_int4: as pa_reshape_and_cache; row x (widened to fp32,
+ * clamped to +-65504) is stored as
+ *   scale = half((max x - min x) / 15), mid = half((max x + min x) * 0.5),
+ *   code  = clamp(rint((x - mid) * (1 / scale) + 7.5), 0, 15)
+ * each operation rounded to nearest in fp32 (rint: ties to even; 1 / scale is 0
+ * when scale is 0, and the row then reads back as mid). A row with a NaN gets
+ * NaN scale and mid, so that it reads back as NaN. src_dtype is the type of key
+ * and value.
+ *
+ * pa_paged_decode_int4: pa_paged_decode over these caches; q and out are of
+ * type dtype (PA_F16 or PA_BF16). Workspace, plan and order as pa_paged_decode.
+ *
+ * pa_read_slots_int4: the inverse of the write, for callers that attend to
+ * cached rows by other means (a prompt's later chunk, a comparison): row t of
+ * key / value becomes the 16-bit values (nearest even) of slot slot_mapping[t];
+ * a negative slot leaves the row as it was, a slot past the pool too, with
+ * PA_DEVERR_SLOT_RANGE. Strides and alignment as in the write.
+ * ------------------------------------------------------------------------- */
+int pa_reshape_and_cache_int4(const void* key, const void* value, int64_t key_token_stride,
+                              int64_t value_token_stride, void* k_cache, void* v_cache,
+                              const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                              int head_dim, int block_size, int num_blocks, int src_dtype,
+                              int* dev_error, void* stream);
+
+int pa_paged_decode_int4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* seq_order, int num_seqs,
+                         int max_context_len, int num_q_heads, int num_kv_heads, int head_dim,
+                         int block_size, int num_blocks, float scale, int partition_tokens,
+                         void* workspace, size_t workspace_bytes, int* dev_error, int dtype,
+                         void* stream);
+
+int pa_read_slots_int4(void* key, void* value, int64_t key_token_stride,
+                       int64_t value_token_stride, const void* k_cache, const void* v_cache,
+                       const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                       int head_dim, int block_size, int num_blocks, int dtype, int* dev_error,
+                       void* stream);
+
+/* ---------------------------------------------------------------------------
+ * pa_rope_and_cache — rotate queries and keys by their positions and store keys
+ * and values in their slots, in one pass.
+ *
+ * The cached keys of the paper's models carry a rotary position embedding
+ * applied when the token is written; the pages leave it to the model. For token
+ * t at position p = positions[t], with R = rotary_dim and the table row
+ * cos_sin[p] = (cos_0 .. cos_{R/2-1}, sin_0 .. sin_{R/2-1}), every query and key
+ * row x becomes
+ *   a' = a * cos_i - b * sin_i,   b' = b * cos_i + a * sin_i
+ * for its pairs (a, b) = (x[i], x[i + R/2]), or (x[2i], x[2i+1]) when
+ * interleaved is 1; elements from R on stay. fp32, each operation rounded to
+ * nearest by itself. Rotated queries go to q_out (nearest even), rotated keys
+ * and unrotated values to slot_mapping[t] of the caches:
+ *   pa_rope_and_cache       caches of the rows' own type (nearest even)
+ *   pa_rope_and_cache_fp8   E4M3 caches, codes of x' / k_scale and v / v_scale as
+ *                           pa_reshape_and_cache_fp8 takes them, from the fp32 x'
+ *   pa_rope_and_cache_int4  4-bit caches, rows quantized as
+ *                           pa_reshape_and_cache_int4 does, from the fp32 x'
+ *
+ *   q, q_out      device, [num_tokens][num_q_heads][head_dim] with token strides
+ *                 of >= num_q_heads*head_dim elements, a multiple of 8; 16-byte
+ *                 aligned. q_out may be q (equal strides), else must not overlap it
+ *   key, value    as in pa_reshape_and_cache; not modified
+ *   positions     device, int64 [num_tokens]; a position outside
+ *                 [0, num_positions) sets PA_DEVERR_POSITION and nothing of that
+ *                 token is written, neither q_out nor the caches
+ *   cos_sin       device, float [num_positions][rotary_dim], 16-byte aligned
+ *                 (pa_rope_table fills one for plain frequencies; scaled or
+ *                 extended ones are the caller's to compute)
+ *   rotary_dim    a multiple of 16 from 16 to head_dim
+ *   slot_mapping  as in pa_reshape_and_cache; a token with a negative slot (or
+ *                 one past the pool, PA_DEVERR_SLOT_RANGE) has its query rotated
+ *                 and nothing cached
+ * num_q_heads may be any positive number. num_tokens == 0 is a no-op.
+ * ------------------------------------------------------------------------- */
+int pa_rope_and_cache(void* q_out, const void* q, const void* key, const void* value,
+                      int64_t q_out_token_stride, int64_t q_token_stride,
+                      int64_t key_token_stride, int64_t value_token_stride,
+                      const int64_t* positions, const float* cos_sin, int num_positions,
+                      int rotary_dim, int interleaved, void* k_cache, void* v_cache,
+                      const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                      int num_kv_heads, int head_dim, int block_size, int num_blocks, int dtype,
+                      int* dev_error, void* stream);
+
+int pa_rope_and_cache_fp8(void* q_out, const void* q, const void* key, const void* value,
+                          int64_t q_out_token_stride, int64_t q_token_stride,
+                          int64_t key_token_stride, int64_t value_token_stride,
+                          const int64_t* positions, const float* cos_sin, int num_positions,
+                          int rotary_dim, int interleaved, void* k_cache, void* v_cache,
+                          const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                          int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                          int dtype, float k_scale, float v_scale, int* dev_error, void* stream);
+
+int pa_rope_and_cache_int4(void* q_out, const void* q, const void* key, const void* value,
+                           int64_t q_out_token_stride, int64_t q_token_stride,
+                           int64_t key_token_stride, int64_t value_token_stride,
+                           const int64_t* positions, const float* cos_sin, int num_positions,
+                           int rotary_dim, int interleaved, void* k_cache, void* v_cache,
+                           const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                           int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                           int dtype, int* dev_error, void* stream);
+
+/* Host helper: fills cos_sin[num_positions][rotary_dim] (host memory) for the
+ * frequencies theta^(-2i / rotary_dim), angles and functions in double
+ * precision, rounded to float. */
+int pa_rope_table(float* cos_sin, int num_positions, int rotary_dim, double theta);
 
 /* ---------------------------------------------------------------------------
  * pa_paged_decode — decode-step attention through the block tables.

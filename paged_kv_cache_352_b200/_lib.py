@@ -29,12 +29,14 @@ PA_ERR_SEQ_SWAPPED = 7
 PA_F16 = 0
 PA_BF16 = 1
 PA_FP8_E4M3 = 2
+PA_INT4 = 3
 
 PA_DEVERR_SLOT_RANGE = 1
 PA_DEVERR_BLOCK_RANGE = 2
 PA_DEVERR_CONTEXT_RANGE = 4
 PA_DEVERR_WAIT_TIMEOUT = 8
 PA_DEVERR_GROUP = 16
+PA_DEVERR_POSITION = 32
 
 BLOCK_SIZE = 16
 
@@ -48,6 +50,7 @@ class PAError(RuntimeError):
 _c_int = ctypes.c_int
 _c_i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
+_ROPE_ARGS = [_vp] * 4 + [_c_i64] * 4 + [_vp, _vp] + [_c_int] * 3 + [_vp] * 3 + [_c_int] * 7
 _SIGS = {
     "pa_last_error": (ctypes.c_char_p, []),
     "pa_version": (_c_int, []),
@@ -76,6 +79,17 @@ _SIGS = {
                                      _c_int, _c_int, _c_int, _c_int, _c_int, ctypes.c_float,
                                      ctypes.c_float, ctypes.c_float, _c_int, _vp, ctypes.c_size_t,
                                      _vp, _c_int, _vp]),
+    "pa_reshape_and_cache_int4": (_c_int, [_vp, _vp, _c_i64, _c_i64, _vp, _vp, _vp, _c_int,
+                                           _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
+    "pa_read_slots_int4": (_c_int, [_vp, _vp, _c_i64, _c_i64, _vp, _vp, _vp, _c_int, _c_int,
+                                    _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
+    "pa_paged_decode_int4": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int,
+                                      _c_int, _c_int, _c_int, _c_int, _c_int, ctypes.c_float,
+                                      _c_int, _vp, ctypes.c_size_t, _vp, _c_int, _vp]),
+    "pa_rope_and_cache": (_c_int, _ROPE_ARGS + [_vp, _vp]),
+    "pa_rope_and_cache_fp8": (_c_int, _ROPE_ARGS + [ctypes.c_float, ctypes.c_float, _vp, _vp]),
+    "pa_rope_and_cache_int4": (_c_int, _ROPE_ARGS + [_vp, _vp]),
+    "pa_rope_table": (_c_int, [_vp, _c_int, _c_int, ctypes.c_double]),
     "pa_paged_decode_cascade_workspace_size": (_c_int, [_c_int] * 10 +
                                                 [ctypes.POINTER(ctypes.c_size_t)]),
     "pa_paged_decode_cascade": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int,
@@ -226,6 +240,49 @@ def _cache_dims(k_cache, v_cache):
     return nb, hkv, bs, d
 
 
+def _pool_dims(k_cache, v_cache):
+    """(num_blocks, num_kv_heads, block_size, head_dim, dtype code) of a pool to move whole
+    blocks of. A uint8 pool holds 4-bit rows when its last dimension is a 4-bit row's
+    (head_dim/2 + 4 bytes: 36 or 68), else E4M3 codes."""
+    nb, hkv, bs, d = _cache_dims(k_cache, v_cache)
+    if k_cache.dtype == _torch().uint8 and d in (36, 68):
+        return nb, hkv, bs, 2 * (d - 4), PA_INT4
+    return nb, hkv, bs, d, dtype_code(k_cache)
+
+
+def _int4_dims(k_cache, v_cache):
+    nb, hkv, bs, d, code = _pool_dims(k_cache, v_cache)
+    if code != PA_INT4:
+        raise PAError(PA_ERR_INVALID_ARG, "k_cache/v_cache must be uint8 [num_blocks, "
+                                          "num_kv_heads, block_size, head_dim/2 + 4] with "
+                                          "head_dim 64 or 128")
+    return nb, hkv, bs, d
+
+
+def _check_rows(key, value, hkv, d):
+    T = key.shape[0]
+    if key.shape[1:] != (hkv, d) or value.shape[1:] != (hkv, d) or value.shape[0] != T:
+        raise PAError(PA_ERR_INVALID_ARG, "key/value must be [T, num_kv_heads, head_dim]")
+    for x in (key, value):
+        if T and (x.stride(2) != 1 or (hkv > 1 and x.stride(1) != d)):
+            raise PAError(PA_ERR_INVALID_ARG, "key/value rows must be dense per token")
+    if value.dtype != key.dtype:
+        raise PAError(PA_ERR_INVALID_ARG, "value must be of key's dtype")
+    return T
+
+
+def _token_stride(x):
+    """Token stride of a [T, H, d] tensor: that of a dense one when T is 1, where a tensor's own
+    may be anything."""
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def _same_device(*tensors):
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise PAError(PA_ERR_INVALID_ARG, f"tensors on different devices: {sorted(map(str, devs))}")
+
+
 # --------------------------------------------------------------------------
 # device calls
 # --------------------------------------------------------------------------
@@ -253,12 +310,12 @@ def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, dev_error=N
 
 def pa_copy_blocks(k_cache, v_cache, pairs, stream=None):
     """Copy blocks ``pairs[i, 0] -> pairs[i, 1]`` (host int64 array ``[n, 2]``)."""
-    nb, hkv, bs, d = _cache_dims(k_cache, v_cache)
+    nb, hkv, bs, d, code = _pool_dims(k_cache, v_cache)
     p = np.ascontiguousarray(np.asarray(pairs, dtype=np.int64).reshape(-1, 2))
     with _device(k_cache):
         _check(lib().pa_copy_blocks(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
                                     p.ctypes.data if len(p) else None, len(p), hkv, d, bs, nb,
-                                    dtype_code(k_cache), _stream(stream)))
+                                    code, _stream(stream)))
 
 
 def _pool_ptr(t, name):
@@ -273,8 +330,8 @@ def _pool_ptr(t, name):
 def pa_swap_blocks(src_k, src_v, dst_k, dst_v, pairs, stream=None):
     """Copy blocks ``pairs[i, 0]`` of the source pool over ``pairs[i, 1]`` of the
     destination pool; pools are CUDA tensors or pinned host tensors."""
-    s_nb, hkv, bs, d = _cache_dims(src_k, src_v)
-    d_nb, hkv2, bs2, d2 = _cache_dims(dst_k, dst_v)
+    s_nb, hkv, bs, d, code = _pool_dims(src_k, src_v)
+    d_nb, hkv2, bs2, d2, _ = _pool_dims(dst_k, dst_v)
     if (hkv, bs, d) != (hkv2, bs2, d2) or src_k.dtype != dst_k.dtype:
         raise PAError(PA_ERR_INVALID_ARG, "source and destination pools differ in layout")
     p = np.ascontiguousarray(np.asarray(pairs, dtype=np.int64).reshape(-1, 2))
@@ -282,7 +339,7 @@ def pa_swap_blocks(src_k, src_v, dst_k, dst_v, pairs, stream=None):
         _check(lib().pa_swap_blocks(_pool_ptr(src_k, "src_k"), _pool_ptr(src_v, "src_v"), s_nb,
                                     _pool_ptr(dst_k, "dst_k"), _pool_ptr(dst_v, "dst_v"), d_nb,
                                     p.ctypes.data if len(p) else None, len(p), hkv, d, bs,
-                                    dtype_code(src_k), _stream(stream)))
+                                    code, _stream(stream)))
 
 
 def pa_paged_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
@@ -437,6 +494,139 @@ def pa_paged_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, ma
             float(k_scale), float(v_scale), int(partition_tokens), _dev_ptr(workspace, "workspace"),
             ws_bytes, _dev_ptr(dev_error, "dev_error", torch.int32), dtype_code(q),
             _stream(stream)))
+
+
+def pa_reshape_and_cache_int4(key, value, k_cache, v_cache, slot_mapping, dev_error=None,
+                              stream=None):
+    """Quantize ``key``/``value`` ``[T, num_kv_heads, head_dim]`` (float16/bfloat16)
+    into the 4-bit caches (uint8 ``[num_blocks, num_kv_heads, 16, head_dim/2 + 4]``)
+    at ``slot_mapping`` (int64 [T])."""
+    torch = _torch()
+    nb, hkv, bs, d = _int4_dims(k_cache, v_cache)
+    T = _check_rows(key, value, hkv, d)
+    if slot_mapping.shape != (T,):
+        raise PAError(PA_ERR_INVALID_ARG, "slot_mapping must be [T]")
+    _same_device(key, value, k_cache, v_cache, slot_mapping, dev_error)
+    with _device(k_cache):
+        _check(lib().pa_reshape_and_cache_int4(
+            _dev_ptr(key, "key", contiguous=False), _dev_ptr(value, "value", contiguous=False),
+            _token_stride(key), _token_stride(value), _dev_ptr(k_cache, "k_cache"),
+            _dev_ptr(v_cache, "v_cache"), _dev_ptr(slot_mapping, "slot_mapping", torch.int64), T,
+            hkv, d, bs, nb, dtype_code(key), _dev_ptr(dev_error, "dev_error", torch.int32),
+            _stream(stream)))
+
+
+def pa_read_slots_int4(key, value, k_cache, v_cache, slot_mapping, dev_error=None, stream=None):
+    """Write the values held at ``slot_mapping`` (int64 [T]) of 4-bit caches into
+    ``key``/``value`` ``[T, num_kv_heads, head_dim]`` (float16/bfloat16); rows with a
+    negative slot stay as they were."""
+    torch = _torch()
+    nb, hkv, bs, d = _int4_dims(k_cache, v_cache)
+    T = _check_rows(key, value, hkv, d)
+    if slot_mapping.shape != (T,):
+        raise PAError(PA_ERR_INVALID_ARG, "slot_mapping must be [T]")
+    _same_device(key, value, k_cache, v_cache, slot_mapping, dev_error)
+    with _device(k_cache):
+        _check(lib().pa_read_slots_int4(
+            _dev_ptr(key, "key", contiguous=False), _dev_ptr(value, "value", contiguous=False),
+            _token_stride(key), _token_stride(value), _dev_ptr(k_cache, "k_cache"),
+            _dev_ptr(v_cache, "v_cache"), _dev_ptr(slot_mapping, "slot_mapping", torch.int64), T,
+            hkv, d, bs, nb, dtype_code(key), _dev_ptr(dev_error, "dev_error", torch.int32),
+            _stream(stream)))
+
+
+def pa_paged_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                         scale, partition_tokens=0, workspace=None, dev_error=None, stream=None,
+                         seq_order=None):
+    """pa_paged_decode over 4-bit caches (uint8 ``[num_blocks, num_kv_heads, 16,
+    head_dim/2 + 4]``); ``q``/``out`` are float16 or bfloat16."""
+    torch = _torch()
+    nb, hkv, bs, d = _int4_dims(k_cache, v_cache)
+    if q.dim() != 3 or q.shape[2] != d or out.shape != q.shape or out.dtype != q.dtype:
+        raise PAError(PA_ERR_INVALID_ARG, "q/out must be [B, num_q_heads, head_dim], one dtype")
+    B, hq, _ = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise PAError(PA_ERR_INVALID_ARG, "block_tables must be [B, max_blocks], context_lens [B]")
+    _same_device(out, q, k_cache, v_cache, block_tables, context_lens, workspace, dev_error,
+                 seq_order)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _device(q):
+        _check(lib().pa_paged_decode_int4(
+            _dev_ptr(out, "out"), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
+            _dev_ptr(v_cache, "v_cache"), _dev_ptr(block_tables, "block_tables", torch.int32),
+            block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
+            _order_ptr(seq_order, B), B, int(max_context_len), hq, hkv, d, bs, nb, float(scale),
+            int(partition_tokens), _dev_ptr(workspace, "workspace"), ws_bytes,
+            _dev_ptr(dev_error, "dev_error", torch.int32), dtype_code(q), _stream(stream)))
+
+
+def pa_rope_table(num_positions, rotary_dim, theta=10000.0) -> np.ndarray:
+    """Host float32 ``[num_positions, rotary_dim]`` cos/sin table for the frequencies
+    ``theta ** (-2 i / rotary_dim)``: ``rotary_dim/2`` cosines, then as many sines."""
+    table = np.empty((int(num_positions), int(rotary_dim)), np.float32)
+    _check(lib().pa_rope_table(table.ctypes.data if table.size else None, int(num_positions),
+                               int(rotary_dim), float(theta)))
+    return table
+
+
+def _rope(call, dims, cache_ok, q_out, q, key, value, positions, cos_sin, k_cache, v_cache,
+          slot_mapping, interleaved, scales, dev_error, stream):
+    torch = _torch()
+    nb, hkv, bs, d = dims
+    T = _check_rows(key, value, hkv, d)
+    if not cache_ok:
+        raise PAError(PA_ERR_INVALID_ARG, "k_cache/v_cache are not of the call's element type")
+    if (q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or q_out.shape != q.shape or
+            q.dtype != key.dtype or q_out.dtype != key.dtype):
+        raise PAError(PA_ERR_INVALID_ARG, "q/q_out must be [T, num_q_heads, head_dim] in key's "
+                                          "dtype")
+    hq = q.shape[1]
+    for x in (q, q_out):
+        if T and (x.stride(2) != 1 or (hq > 1 and x.stride(1) != d)):
+            raise PAError(PA_ERR_INVALID_ARG, "q/q_out rows must be dense per token")
+    if positions.shape != (T,) or slot_mapping.shape != (T,) or cos_sin.dim() != 2:
+        raise PAError(PA_ERR_INVALID_ARG, "positions and slot_mapping must be [T], cos_sin "
+                                          "[num_positions, rotary_dim]")
+    _same_device(q_out, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                 dev_error)
+    with _device(k_cache):
+        _check(call(
+            _dev_ptr(q_out, "q_out", contiguous=False), _dev_ptr(q, "q", contiguous=False),
+            _dev_ptr(key, "key", contiguous=False), _dev_ptr(value, "value", contiguous=False),
+            _token_stride(q_out), _token_stride(q), _token_stride(key), _token_stride(value),
+            _dev_ptr(positions, "positions", torch.int64),
+            _dev_ptr(cos_sin, "cos_sin", torch.float32), cos_sin.shape[0], cos_sin.shape[1],
+            int(bool(interleaved)), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
+            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), T, hq, hkv, d, bs, nb,
+            dtype_code(key), *scales, _dev_ptr(dev_error, "dev_error", torch.int32),
+            _stream(stream)))
+
+
+def pa_rope_and_cache(q_out, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                      interleaved=False, dev_error=None, stream=None):
+    """Rotate ``q`` ``[T, num_q_heads, head_dim]`` into ``q_out`` (may be ``q``) and store
+    the rotated ``key`` and the ``value`` rows ``[T, num_kv_heads, head_dim]`` at
+    ``slot_mapping``. ``positions`` (int64 [T]) index the rows of ``cos_sin`` (float32
+    ``[num_positions, rotary_dim]``, ``pa_rope_table``)."""
+    _rope(lib().pa_rope_and_cache, _cache_dims(k_cache, v_cache), k_cache.dtype == key.dtype,
+          q_out, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping, interleaved,
+          (), dev_error, stream)
+
+
+def pa_rope_and_cache_fp8(q_out, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                          k_scale, v_scale, interleaved=False, dev_error=None, stream=None):
+    """pa_rope_and_cache into E4M3 caches (uint8 / float8_e4m3fn) with key and value scales."""
+    _rope(lib().pa_rope_and_cache_fp8, _cache_dims(k_cache, v_cache),
+          dtype_code(k_cache) == PA_FP8_E4M3, q_out, q, key, value, positions, cos_sin, k_cache,
+          v_cache, slot_mapping, interleaved, (float(k_scale), float(v_scale)), dev_error, stream)
+
+
+def pa_rope_and_cache_int4(q_out, q, key, value, positions, cos_sin, k_cache, v_cache,
+                           slot_mapping, interleaved=False, dev_error=None, stream=None):
+    """pa_rope_and_cache into 4-bit caches (uint8 ``[num_blocks, num_kv_heads, 16,
+    head_dim/2 + 4]``)."""
+    _rope(lib().pa_rope_and_cache_int4, _int4_dims(k_cache, v_cache), True, q_out, q, key, value,
+          positions, cos_sin, k_cache, v_cache, slot_mapping, interleaved, (), dev_error, stream)
 
 
 def pa_paged_decode_cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,

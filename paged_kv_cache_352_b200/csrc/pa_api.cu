@@ -1,12 +1,14 @@
 // C interface of libpa: argument checks on the host, then kernel launches on the
 // caller's stream. Nothing here synchronises or allocates device memory.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 #include <string>
 #include <unordered_set>
 #include <vector>
@@ -35,14 +37,19 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Element bytes of a cache type (PA_F16, PA_BF16: 2; PA_FP8_E4M3: 1).
-int64_t elem_bytes(int dtype) { return dtype == PA_FP8_E4M3 ? 1 : 2; }
+// Bytes of a token's row of one KV head in a cache of this type (PA_F16, PA_BF16:
+// 2 per element; PA_FP8_E4M3: 1; PA_INT4: half a byte and the row's two halves).
+int64_t row_bytes(int head_dim, int dtype) {
+  if (dtype == PA_INT4) return head_dim / 2 + 4;
+  return dtype == PA_FP8_E4M3 ? head_dim : 2 * head_dim;
+}
 
 int check_cache_shape(int num_kv_heads, int head_dim, int block_size, int num_blocks, int dtype,
-                      bool allow_fp8 = false) {
-  if (dtype != PA_F16 && dtype != PA_BF16 && !(allow_fp8 && dtype == PA_FP8_E4M3))
+                      bool allow_codes = false) {
+  if (dtype != PA_F16 && dtype != PA_BF16 &&
+      !(allow_codes && (dtype == PA_FP8_E4M3 || dtype == PA_INT4)))
     return fail(PA_ERR_UNSUPPORTED, "dtype %d: expected PA_F16 or PA_BF16%s", dtype,
-                allow_fp8 ? " or PA_FP8_E4M3" : "");
+                allow_codes ? " or PA_FP8_E4M3 or PA_INT4" : "");
   if (block_size != kBlockSize)
     return fail(PA_ERR_UNSUPPORTED, "block_size %d: only %d is supported", block_size,
                 kBlockSize);
@@ -235,7 +242,7 @@ int pa_copy_blocks(void* k_cache, void* v_cache, const int64_t* pairs, int num_p
     if (srcs.count(d))
       return fail(PA_ERR_INVALID_ARG, "block %lld is both a source and a destination",
                   (long long)d);
-  const int64_t block_bytes = (int64_t)num_kv_heads * kBlockSize * head_dim * elem_bytes(dtype);
+  const int64_t block_bytes = (int64_t)num_kv_heads * kBlockSize * row_bytes(head_dim, dtype);
   for (int first = 0; first < num_pairs; first += kMaxCopyPairsPerLaunch) {
     const int n = std::min(kMaxCopyPairsPerLaunch, num_pairs - first);
     CopyPairs cp;
@@ -282,7 +289,7 @@ int pa_swap_blocks(const void* src_k, const void* src_v, int src_num_blocks, voi
   if (int st = device_view(src_v, "src_v", &sv)) return st;
   if (int st = device_view(dst_k, "dst_k", &dk)) return st;
   if (int st = device_view(dst_v, "dst_v", &dv)) return st;
-  const int64_t block_bytes = (int64_t)num_kv_heads * kBlockSize * head_dim * elem_bytes(dtype);
+  const int64_t block_bytes = (int64_t)num_kv_heads * kBlockSize * row_bytes(head_dim, dtype);
   for (int first = 0; first < num_pairs; first += kMaxCopyPairsPerLaunch) {
     const int n = std::min(kMaxCopyPairsPerLaunch, num_pairs - first);
     CopyPairs cp;
@@ -377,8 +384,8 @@ int pa_cascade_order(const int32_t* context_lens, const int32_t* seq_group,
 
 namespace {
 
-// pa_paged_decode over a cache of type cache_dtype (dtype itself, or E4M3 with
-// key and value scales).
+// pa_paged_decode over a cache of type cache_dtype (dtype itself, E4M3 with key
+// and value scales, or 4-bit codes).
 int paged_decode_impl(void* out, const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_tables, int max_blocks_per_seq,
                       const int32_t* context_lens, const int32_t* seq_order, int num_seqs,
@@ -879,5 +886,234 @@ int pa_reshape_and_cache_fp8(const void* key, const void* value, int64_t key_tok
                                    static_cast<cudaStream_t>(stream)),
       "reshape_and_cache_fp8 launch");
 }
+
+int pa_paged_decode_int4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* seq_order, int num_seqs,
+                         int max_context_len, int num_q_heads, int num_kv_heads, int head_dim,
+                         int block_size, int num_blocks, float scale, int partition_tokens,
+                         void* workspace, size_t workspace_bytes, int* dev_error, int dtype,
+                         void* stream) {
+  const NvtxRange nvtx_range("pa_paged_decode_int4");
+  clear_error();
+  return paged_decode_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                           context_lens, seq_order, num_seqs, max_context_len, num_q_heads,
+                           num_kv_heads, head_dim, block_size, num_blocks, scale, 1.f, 1.f,
+                           partition_tokens, workspace, workspace_bytes, dev_error, dtype, PA_INT4,
+                           stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The arguments that the rotary writes and the 4-bit write and read-back share.
+// rows: query heads (0 when the call takes no queries) and KV heads.
+int check_token_rows(const void* key, const void* value, int64_t key_stride, int64_t value_stride,
+                     const void* k_cache, const void* v_cache, const int64_t* slot_mapping,
+                     int num_kv_heads, int head_dim) {
+  if (!key || !value || !k_cache || !v_cache || !slot_mapping)
+    return fail(PA_ERR_INVALID_ARG, "null pointer argument");
+  const int64_t row = (int64_t)num_kv_heads * head_dim;
+  if (key_stride < row || value_stride < row || key_stride % 8 || value_stride % 8)
+    return fail(PA_ERR_INVALID_ARG,
+                "token strides (%lld, %lld) must be >= num_kv_heads*head_dim (%lld) and a "
+                "multiple of 8",
+                (long long)key_stride, (long long)value_stride, (long long)row);
+  if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(PA_ERR_INVALID_ARG, "key, value and cache pointers must be 16-byte aligned");
+  return PA_OK;
+}
+
+int rope_and_cache_impl(void* q_out, const void* q, const void* key, const void* value,
+                        int64_t q_out_token_stride, int64_t q_token_stride,
+                        int64_t key_token_stride, int64_t value_token_stride,
+                        const int64_t* positions, const float* cos_sin, int num_positions,
+                        int rotary_dim, int interleaved, void* k_cache, void* v_cache,
+                        const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                        int num_kv_heads, int head_dim, int block_size, int num_blocks, int dtype,
+                        int cache_dtype, float k_scale, float v_scale, int* dev_error,
+                        void* stream) {
+  if (int st = check_cache_shape(num_kv_heads, head_dim, block_size, num_blocks, dtype)) return st;
+  if (num_q_heads <= 0) return fail(PA_ERR_INVALID_ARG, "num_q_heads must be positive");
+  if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16)
+    return fail(PA_ERR_UNSUPPORTED,
+                "rotary_dim %d: expected a multiple of 16 from 16 to head_dim (%d)", rotary_dim,
+                head_dim);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(PA_ERR_INVALID_ARG, "interleaved %d: expected 0 or 1", interleaved);
+  if (num_positions <= 0) return fail(PA_ERR_INVALID_ARG, "num_positions must be positive");
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (num_tokens == 0) return PA_OK;
+  if (!q_out || !q || !positions || !cos_sin)
+    return fail(PA_ERR_INVALID_ARG, "null pointer argument");
+  const int64_t row = (int64_t)num_q_heads * head_dim;
+  if (q_token_stride < row || q_out_token_stride < row || q_token_stride % 8 ||
+      q_out_token_stride % 8)
+    return fail(PA_ERR_INVALID_ARG,
+                "query token strides (%lld, %lld) must be >= num_q_heads*head_dim (%lld) and a "
+                "multiple of 8",
+                (long long)q_token_stride, (long long)q_out_token_stride, (long long)row);
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(cos_sin))
+    return fail(PA_ERR_INVALID_ARG, "q, q_out and cos_sin must be 16-byte aligned");
+  // q_out is q itself (each element is read before it is written) or apart from it
+  if (q_out == q && q_out_token_stride != q_token_stride)
+    return fail(PA_ERR_INVALID_ARG, "q_out == q needs equal token strides");
+  if (int st = check_token_rows(key, value, key_token_stride, value_token_stride, k_cache, v_cache,
+                                slot_mapping, num_kv_heads, head_dim))
+    return st;
+  RopeArgs r;
+  r.q_out = q_out;
+  r.q = q;
+  r.key = key;
+  r.value = value;
+  r.q_out_stride = q_out_token_stride;
+  r.q_stride = q_token_stride;
+  r.key_stride = key_token_stride;
+  r.value_stride = value_token_stride;
+  r.positions = positions;
+  r.cos_sin = cos_sin;
+  r.k_cache = k_cache;
+  r.v_cache = v_cache;
+  r.slot_mapping = slot_mapping;
+  r.dev_error = dev_error;
+  r.num_slots = (int64_t)num_blocks * kBlockSize;
+  r.num_positions = num_positions;
+  r.num_tokens = num_tokens;
+  r.num_q_heads = num_q_heads;
+  r.num_kv_heads = num_kv_heads;
+  r.rotary_dim = rotary_dim;
+  r.interleaved = interleaved;
+  r.k_scale = k_scale;
+  r.v_scale = v_scale;
+  return cuda_status(launch_rope_and_cache(r, head_dim, dtype, cache_dtype,
+                                           static_cast<cudaStream_t>(stream)),
+                     "rope_and_cache launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_reshape_and_cache_int4(const void* key, const void* value, int64_t key_token_stride,
+                              int64_t value_token_stride, void* k_cache, void* v_cache,
+                              const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                              int head_dim, int block_size, int num_blocks, int src_dtype,
+                              int* dev_error, void* stream) {
+  const NvtxRange nvtx_range("pa_reshape_and_cache_int4");
+  clear_error();
+  if (int st = check_cache_shape(num_kv_heads, head_dim, block_size, num_blocks, src_dtype))
+    return st;
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (num_tokens == 0) return PA_OK;
+  if (int st = check_token_rows(key, value, key_token_stride, value_token_stride, k_cache, v_cache,
+                                slot_mapping, num_kv_heads, head_dim))
+    return st;
+  RopeArgs r{};
+  r.key = key;
+  r.value = value;
+  r.key_stride = key_token_stride;
+  r.value_stride = value_token_stride;
+  r.k_cache = k_cache;
+  r.v_cache = v_cache;
+  r.slot_mapping = slot_mapping;
+  r.dev_error = dev_error;
+  r.num_slots = (int64_t)num_blocks * kBlockSize;
+  r.num_tokens = num_tokens;
+  r.num_kv_heads = num_kv_heads;
+  return cuda_status(launch_rope_and_cache(r, head_dim, src_dtype, PA_INT4,
+                                           static_cast<cudaStream_t>(stream)),
+                     "reshape_and_cache_int4 launch");
+}
+
+int pa_read_slots_int4(void* key, void* value, int64_t key_token_stride,
+                       int64_t value_token_stride, const void* k_cache, const void* v_cache,
+                       const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                       int head_dim, int block_size, int num_blocks, int dtype, int* dev_error,
+                       void* stream) {
+  const NvtxRange nvtx_range("pa_read_slots_int4");
+  clear_error();
+  if (int st = check_cache_shape(num_kv_heads, head_dim, block_size, num_blocks, dtype)) return st;
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (num_tokens == 0) return PA_OK;
+  if (int st = check_token_rows(key, value, key_token_stride, value_token_stride, k_cache, v_cache,
+                                slot_mapping, num_kv_heads, head_dim))
+    return st;
+  return cuda_status(
+      launch_read_slots_int4(key, value, key_token_stride, value_token_stride, k_cache, v_cache,
+                             slot_mapping, num_tokens, num_kv_heads, head_dim, num_blocks, dtype,
+                             dev_error, static_cast<cudaStream_t>(stream)),
+      "read_slots_int4 launch");
+}
+
+int pa_rope_table(float* cos_sin, int num_positions, int rotary_dim, double theta) {
+  clear_error();
+  if (num_positions < 0) return fail(PA_ERR_INVALID_ARG, "num_positions must be >= 0");
+  if (rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16)
+    return fail(PA_ERR_UNSUPPORTED, "rotary_dim %d: expected a multiple of 16 from 16 to 128",
+                rotary_dim);
+  if (!(theta > 0.0) || !(theta <= 1e300))
+    return fail(PA_ERR_INVALID_ARG, "theta must be positive and finite");
+  if (num_positions == 0) return PA_OK;
+  if (!cos_sin) return fail(PA_ERR_INVALID_ARG, "null pointer argument");
+  const int half = rotary_dim / 2;
+  for (int i = 0; i < half; ++i) {
+    const double f = std::pow(theta, -2.0 * i / rotary_dim);
+    for (int64_t p = 0; p < num_positions; ++p) {
+      const double a = (double)p * f;
+      cos_sin[p * rotary_dim + i] = (float)std::cos(a);
+      cos_sin[p * rotary_dim + half + i] = (float)std::sin(a);
+    }
+  }
+  return PA_OK;
+}
+
+#define PA_ROPE_ARGS                                                                             \
+  q_out, q, key, value, q_out_token_stride, q_token_stride, key_token_stride, value_token_stride, \
+      positions, cos_sin, num_positions, rotary_dim, interleaved, k_cache, v_cache, slot_mapping, \
+      num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, dtype
+
+int pa_rope_and_cache(void* q_out, const void* q, const void* key, const void* value,
+                      int64_t q_out_token_stride, int64_t q_token_stride,
+                      int64_t key_token_stride, int64_t value_token_stride,
+                      const int64_t* positions, const float* cos_sin, int num_positions,
+                      int rotary_dim, int interleaved, void* k_cache, void* v_cache,
+                      const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                      int num_kv_heads, int head_dim, int block_size, int num_blocks, int dtype,
+                      int* dev_error, void* stream) {
+  const NvtxRange nvtx_range("pa_rope_and_cache");
+  clear_error();
+  return rope_and_cache_impl(PA_ROPE_ARGS, dtype, 1.f, 1.f, dev_error, stream);
+}
+
+int pa_rope_and_cache_fp8(void* q_out, const void* q, const void* key, const void* value,
+                          int64_t q_out_token_stride, int64_t q_token_stride,
+                          int64_t key_token_stride, int64_t value_token_stride,
+                          const int64_t* positions, const float* cos_sin, int num_positions,
+                          int rotary_dim, int interleaved, void* k_cache, void* v_cache,
+                          const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                          int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                          int dtype, float k_scale, float v_scale, int* dev_error, void* stream) {
+  const NvtxRange nvtx_range("pa_rope_and_cache_fp8");
+  clear_error();
+  if (!positive_finite(k_scale) || !positive_finite(v_scale))
+    return fail(PA_ERR_INVALID_ARG, "k_scale and v_scale must be finite and positive");
+  return rope_and_cache_impl(PA_ROPE_ARGS, PA_FP8_E4M3, k_scale, v_scale, dev_error, stream);
+}
+
+int pa_rope_and_cache_int4(void* q_out, const void* q, const void* key, const void* value,
+                           int64_t q_out_token_stride, int64_t q_token_stride,
+                           int64_t key_token_stride, int64_t value_token_stride,
+                           const int64_t* positions, const float* cos_sin, int num_positions,
+                           int rotary_dim, int interleaved, void* k_cache, void* v_cache,
+                           const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                           int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                           int dtype, int* dev_error, void* stream) {
+  const NvtxRange nvtx_range("pa_rope_and_cache_int4");
+  clear_error();
+  return rope_and_cache_impl(PA_ROPE_ARGS, PA_INT4, 1.f, 1.f, dev_error, stream);
+}
+
+#undef PA_ROPE_ARGS
 
 }  // extern "C"

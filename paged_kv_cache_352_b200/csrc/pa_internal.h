@@ -135,7 +135,8 @@ cudaError_t launch_cascade_decode(const DecodeArgs& pre, const DecodeArgs& own, 
                                   int g_own, int dtype, int cache_dtype, cudaStream_t stream);
 bool cascade_single_launch(int head_dim, int g_own, int stacked, int dtype, int cache_dtype);
 
-// dtype: query/output type (PA_F16 or PA_BF16); cache_dtype: dtype or PA_FP8_E4M3.
+// dtype: query/output type (PA_F16 or PA_BF16); cache_dtype: dtype, PA_FP8_E4M3 or
+// PA_INT4.
 cudaError_t launch_paged_decode(const DecodeArgs& a, int head_dim, int group, int dtype,
                                 int cache_dtype, cudaStream_t stream);
 
@@ -153,6 +154,34 @@ cudaError_t launch_reshape_and_cache_fp8(const void* key, const void* value, int
                                          int num_kv_heads, int head_dim, int num_blocks,
                                          int src_dtype, float k_scale, float v_scale,
                                          int* dev_error, cudaStream_t stream);
+
+// Rotary and 4-bit cache writes. Strides in elements; cache_dtype is the type of
+// q/key/value (`dtype`), PA_FP8_E4M3 or PA_INT4.
+struct RopeArgs {
+  void* q_out;
+  const void* q;
+  const void* key;
+  const void* value;
+  int64_t q_out_stride, q_stride, key_stride, value_stride;
+  const int64_t* positions;
+  const float* cos_sin;  // [num_positions][rotary_dim]
+  void* k_cache;
+  void* v_cache;
+  const int64_t* slot_mapping;
+  int* dev_error;
+  int64_t num_slots, num_positions;
+  int num_tokens, num_q_heads, num_kv_heads, rotary_dim, interleaved;
+  float k_scale, v_scale;
+};
+// rotary_dim == 0 with no query heads: the plain write into a 4-bit cache.
+cudaError_t launch_rope_and_cache(const RopeArgs& r, int head_dim, int dtype, int cache_dtype,
+                                  cudaStream_t stream);
+
+cudaError_t launch_read_slots_int4(void* key, void* value, int64_t key_stride,
+                                   int64_t value_stride, const void* k_cache, const void* v_cache,
+                                   const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                                   int head_dim, int num_blocks, int dtype, int* dev_error,
+                                   cudaStream_t stream);
 
 // Cascade decode of sequences that share leading blocks: the prefix states of
 // every group come from one decode over the shared blocks (the members' query

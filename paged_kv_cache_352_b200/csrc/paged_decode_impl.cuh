@@ -1,6 +1,7 @@
 // Paged-decode kernel template and its launcher, instantiated once per
 // (storage type, head_dim) in paged_decode_<type>_d<dim>.cu, and per
-// (query type, head_dim) over E4M3 caches in paged_decode_<type>_d<dim>_e4m3.cu.
+// (query type, head_dim) over E4M3 caches in paged_decode_<type>_d<dim>_e4m3.cu
+// and over 4-bit caches in paged_decode_<type>_d<dim>_int4.cu.
 #pragma once
 
 #include <cuda.h>
@@ -17,6 +18,7 @@
 #include "decode_merge.cuh"
 #include "decode_policies.cuh"
 #include "decode_policy_fp8.cuh"
+#include "decode_policy_int4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -842,7 +844,9 @@ bool use_tensor_path_e4m3(int group) {
 
 template <typename T, int D, int G, typename C>
 cudaError_t launch_g(const DecodeArgs& a, int dtype, cudaStream_t stream) {
-  if constexpr (std::is_same<C, E4M3>::value) {
+  if constexpr (std::is_same<C, Int4>::value) {
+    return launch_kernel<Int4TensorPolicy<T, D, G>, T, D, G, 4, 4>(a, dtype, stream);
+  } else if constexpr (std::is_same<C, E4M3>::value) {
     if constexpr (G == 8) {
       // warp-per-partition split over 8 query heads per KV head: two blocks per
       // loop step (long-context 8-bit batch 237.6 -> 227.2 us); PA_DECODE_TILE
@@ -869,8 +873,8 @@ template <typename T, int D, typename C>
 cudaError_t launch_group(const DecodeArgs& a, int group, int dtype, cudaStream_t stream) {
   switch (group) {
     case 1:
-      if constexpr (std::is_same<C, E4M3>::value) return launch_g<T, D, 1, C>(a, dtype, stream);
-      return launch_tiles<CudaCorePolicy<T, D, 1, C>, T, D, 1>(a, dtype, stream);
+      if constexpr (!std::is_same<C, T>::value) return launch_g<T, D, 1, C>(a, dtype, stream);
+      else return launch_tiles<CudaCorePolicy<T, D, 1, C>, T, D, 1>(a, dtype, stream);
     case 2: return launch_g<T, D, 2, C>(a, dtype, stream);
     case 4: return launch_g<T, D, 4, C>(a, dtype, stream);
     case 8: return launch_g<T, D, 8, C>(a, dtype, stream);
@@ -916,7 +920,7 @@ cudaError_t launch_cascade_typed(const DecodeArgs& pre, const DecodeArgs& own, i
 }
 
 // Launches the decode kernel for one query/output type T, head_dim and cache
-// element type C (T itself, or E4M3).
+// element type C (T itself, E4M3 or Int4).
 template <typename T, int D, typename C = T>
 cudaError_t launch_decode_typed(const DecodeArgs& a, int group, int dtype,
                                 cudaStream_t stream) {
