@@ -162,4 +162,33 @@ __device__ __forceinline__ void finish_partition(const DecodeArgs& a, float* wts
   __syncthreads();
 }
 
+// The warp-per-partition split's counterpart: merges the warps' states (WARPS
+// consecutive partitions, as above in shared memory) into row `row` of the
+// sequence's states in the workspace. Every thread of the CTA calls it.
+template <int D, int G, int WARPS>
+__device__ __forceinline__ void store_cta_state(const DecodeArgs& a, const float* red_m,
+                                                const float* red_l, const float* red_acc, int s,
+                                                int kvh, int row) {
+  const size_t row0 = (((size_t)s * a.num_kv_heads + kvh) * a.max_parts + row) * G;
+  for (int item = threadIdx.x; item < G * D; item += blockDim.x) {
+    const int g = item / D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, red_m[w * G + g]);
+    const float Mref = M == -INFINITY ? 0.f : M;
+    float L = 0.f, A = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float sc = exp2f(red_m[w * G + g] - Mref);
+      L = fmaf(sc, red_l[w * G + g], L);
+      A = fmaf(sc, red_acc[(w * G) * D + item], A);
+    }
+    a.ws_acc[(row0 + g) * D + (item % D)] = A;
+    if (item % D == 0) {
+      a.ws_m[row0 + g] = M;
+      a.ws_l[row0 + g] = L;
+    }
+  }
+}
+
 }  // namespace pa

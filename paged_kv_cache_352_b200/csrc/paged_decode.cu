@@ -30,13 +30,11 @@
 // E4M3 caches (8-bit codes with a key and a value scale) run the same kernel:
 // the key scale folds into the softmax scale, the value scale multiplies the
 // normalised output, and tiles are widened from codes on the chip. 4-bit caches
-// run it too, with their tokens' own scales applied by the arithmetic policy
-// (decode_policy_int4.cuh).
+// have a kernel of their own (decode_int4.cuh) over the same grid and merges.
 //
 // The kernel template lives in paged_decode_impl.cuh and is instantiated once
 // per (storage type, head_dim) in paged_decode_<type>_d<dim>.cu and once per
-// (query type, head_dim) over E4M3 caches in paged_decode_<type>_d<dim>_e4m3.cu
-// and over 4-bit caches in paged_decode_<type>_d<dim>_int4.cu.
+// (query type, head_dim) over E4M3 caches in paged_decode_<type>_d<dim>_e4m3.cu.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -88,18 +86,18 @@ void set_stall_request(unsigned long long wait_limit_ns) { g_stall_request.store
 
 cudaError_t launch_paged_decode(const DecodeArgs& args, int head_dim, int group, int dtype,
                                 int cache_dtype, cudaStream_t stream) {
+  if (cache_dtype == PA_INT4) {  // no on-chip waits: a stall request stays for the next decode
+    if (head_dim != 64 && head_dim != 128) return cudaErrorInvalidValue;
+    if (dtype == PA_F16)
+      return head_dim == 64 ? launch_decode_f16_d64_int4(args, group, stream)
+                            : launch_decode_f16_d128_int4(args, group, stream);
+    return head_dim == 64 ? launch_decode_bf16_d64_int4(args, group, stream)
+                          : launch_decode_bf16_d128_int4(args, group, stream);
+  }
   DecodeArgs a = args;
   if (const unsigned long long ns = take_stall_request()) {
     a.stall_first_block = 1;
     a.wait_limit_ns = ns;
-  }
-  if (cache_dtype == PA_INT4) {
-    if (head_dim != 64 && head_dim != 128) return cudaErrorInvalidValue;
-    if (dtype == PA_F16)
-      return head_dim == 64 ? launch_decode_f16_d64_int4(a, group, stream)
-                            : launch_decode_f16_d128_int4(a, group, stream);
-    return head_dim == 64 ? launch_decode_bf16_d64_int4(a, group, stream)
-                          : launch_decode_bf16_d128_int4(a, group, stream);
   }
   const bool fp8 = cache_dtype == PA_FP8_E4M3;
   if (!fp8 && cache_dtype != dtype) return cudaErrorInvalidValue;

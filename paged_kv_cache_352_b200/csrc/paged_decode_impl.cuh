@@ -1,7 +1,6 @@
 // Paged-decode kernel template and its launcher, instantiated once per
 // (storage type, head_dim) in paged_decode_<type>_d<dim>.cu, and per
-// (query type, head_dim) over E4M3 caches in paged_decode_<type>_d<dim>_e4m3.cu
-// and over 4-bit caches in paged_decode_<type>_d<dim>_int4.cu.
+// (query type, head_dim) over E4M3 caches in paged_decode_<type>_d<dim>_e4m3.cu.
 #pragma once
 
 #include <cuda.h>
@@ -18,7 +17,6 @@
 #include "decode_merge.cuh"
 #include "decode_policies.cuh"
 #include "decode_policy_fp8.cuh"
-#include "decode_policy_int4.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -557,26 +555,7 @@ __global__ void __launch_bounds__(WARPS * 32, (min_ctas_hint<P, WARPS>()))
   float* red_acc = red_l + WARPS * G;              // [WARPS][G][D]
   pol.to_red(red_m, red_l, red_acc, warp, lane);
   __syncthreads();
-  const size_t row0 = (((size_t)s * a.num_kv_heads + kvh) * a.max_parts + blockIdx.y) * G;
-  for (int item = threadIdx.x; item < G * D; item += blockDim.x) {
-    const int g = item / D;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, red_m[w * G + g]);
-    const float Mref = M == -INFINITY ? 0.f : M;
-    float L = 0.f, A = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float sc = exp2f(red_m[w * G + g] - Mref);
-      L = fmaf(sc, red_l[w * G + g], L);
-      A = fmaf(sc, red_acc[(w * G) * D + item], A);
-    }
-    a.ws_acc[(row0 + g) * D + (item % D)] = A;
-    if (item % D == 0) {
-      a.ws_m[row0 + g] = M;
-      a.ws_l[row0 + g] = L;
-    }
-  }
+  store_cta_state<D, G, WARPS>(a, red_m, red_l, red_acc, s, kvh, blockIdx.y);
 }
 
 constexpr size_t kSmemLimit = 200 * 1024;
@@ -844,9 +823,7 @@ bool use_tensor_path_e4m3(int group) {
 
 template <typename T, int D, int G, typename C>
 cudaError_t launch_g(const DecodeArgs& a, int dtype, cudaStream_t stream) {
-  if constexpr (std::is_same<C, Int4>::value) {
-    return launch_kernel<Int4TensorPolicy<T, D, G>, T, D, G, 4, 4>(a, dtype, stream);
-  } else if constexpr (std::is_same<C, E4M3>::value) {
+  if constexpr (std::is_same<C, E4M3>::value) {
     if constexpr (G == 8) {
       // warp-per-partition split over 8 query heads per KV head: two blocks per
       // loop step (long-context 8-bit batch 237.6 -> 227.2 us); PA_DECODE_TILE
@@ -873,8 +850,8 @@ template <typename T, int D, typename C>
 cudaError_t launch_group(const DecodeArgs& a, int group, int dtype, cudaStream_t stream) {
   switch (group) {
     case 1:
-      if constexpr (!std::is_same<C, T>::value) return launch_g<T, D, 1, C>(a, dtype, stream);
-      else return launch_tiles<CudaCorePolicy<T, D, 1, C>, T, D, 1>(a, dtype, stream);
+      if constexpr (std::is_same<C, E4M3>::value) return launch_g<T, D, 1, C>(a, dtype, stream);
+      return launch_tiles<CudaCorePolicy<T, D, 1, C>, T, D, 1>(a, dtype, stream);
     case 2: return launch_g<T, D, 2, C>(a, dtype, stream);
     case 4: return launch_g<T, D, 4, C>(a, dtype, stream);
     case 8: return launch_g<T, D, 8, C>(a, dtype, stream);
@@ -920,7 +897,7 @@ cudaError_t launch_cascade_typed(const DecodeArgs& pre, const DecodeArgs& own, i
 }
 
 // Launches the decode kernel for one query/output type T, head_dim and cache
-// element type C (T itself, E4M3 or Int4).
+// element type C (T itself, or E4M3).
 template <typename T, int D, typename C = T>
 cudaError_t launch_decode_typed(const DecodeArgs& a, int group, int dtype,
                                 cudaStream_t stream) {
