@@ -1,0 +1,435 @@
+// Beam search's selection (sm_100a): the best continuations over the beams of a
+// sequence and the vocabulary.
+//
+//   score[k][v] = beam_score[k] + x[k][v] - logsumexp_v x[k],
+//   the N largest of the K V scores of a sequence, ties to the smallest k V + v.
+//
+// The logits are read once: 2 or 4 bytes each, against one exponential, a
+// comparison and an addition. A row's ranking does not need its logsumexp, so one
+// kernel takes a tile of a row (kept in registers), leaves the tile's maximum, its
+// sum of exponentials and its N largest logits in the workspace, and a second one
+// per sequence adds up the rows' sums and ranks K x tiles x N candidates.
+//
+// The N largest of a tile without sorting it: the N-th largest of the maxima of
+// kGroups groups of elements bounds the N-th largest element from below, so the few
+// elements at or above it are collected in shared memory and ranked by counting,
+// for each, those before it. Where ties make too many (a tile of equal logits) the N
+// are taken one by one instead; either way the order is (value descending, index
+// ascending), and a result does not depend on the order of the atomics.
+//
+// Scores are formed and ranked in double precision: neighbouring candidates of
+// different beams are often closer than fp32 scores resolve. The exponentials'
+// sums are fp32 per thread (at most kPer terms), double from there on.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr int kBeamThreads = 256;
+constexpr int kGroups = 64;       // groups of a tile whose maxima bound the N-th largest
+constexpr int kTileCap = 1024;    // candidates a tile ranks at once
+constexpr int kMergeThreads = 512;
+constexpr int kMergeCap = 2048;   // candidates a sequence ranks at once
+
+// Floats in the order of unsigned integers (NaN aside).
+__device__ __forceinline__ uint32_t orderable(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_orderable(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// (value, index) as one key: larger is better, ties to the smaller index. 0 is
+// below every candidate.
+__device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
+  return ((uint64_t)orderable(x) << 32) | (uint32_t)~index;
+}
+
+// EPL elements of the logits type per 16-byte load, widened
+template <typename T>
+struct Logits;
+template <>
+struct Logits<float> {
+  static constexpr int kPerLoad = 4;
+  static __device__ __forceinline__ void widen(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
+};
+template <typename T>
+struct Logits {
+  static constexpr int kPerLoad = 8;
+  static __device__ __forceinline__ void widen(const uint4& u, float* f) {
+    Storage<T>::to_f32(u, *reinterpret_cast<float(*)[8]>(f));
+  }
+  static __device__ __forceinline__ float one(const T* p) {
+    return static_cast<float>(*p);
+  }
+};
+
+// One tile of one row: kBeamThreads threads x LOADS 16-byte loads.
+template <typename T, int LOADS>
+__global__ void __launch_bounds__(kBeamThreads)
+    beam_tile_kernel(const T* __restrict__ logits, int64_t row_stride, int vocab, int select,
+                     int tiles, float* __restrict__ tile_max, float* __restrict__ tile_sum,
+                     uint64_t* __restrict__ tile_keys) {
+  grid_dependency_wait();
+  allow_dependents();
+  constexpr int EPL = Logits<T>::kPerLoad;
+  constexpr int kPer = EPL * LOADS;
+  constexpr int kWarps = kBeamThreads / 32;
+  __shared__ uint32_t group_max[kGroups];
+  __shared__ float warp_max[kWarps], warp_sum[kWarps];
+  __shared__ uint64_t cand[kTileCap];
+  __shared__ uint32_t threshold;
+  __shared__ int count;
+  const int tile = blockIdx.x, row = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* x = logits + (int64_t)row * row_stride;
+  const int base = tile * kBeamThreads * kPer;
+  // element e of load i of this thread: index base + (i * kBeamThreads + thread) EPL + e;
+  // past the row: -inf, which is never a candidate and adds nothing
+  float f[kPer];
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    const int at = base + (i * kBeamThreads + (int)threadIdx.x) * EPL;
+    if (at + EPL <= vocab) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + at));
+      Logits<T>::widen(u, f + i * EPL);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e)
+        f[i * EPL + e] = at + e < vocab ? Logits<T>::one(x + at + e) : -INFINITY;
+    }
+  }
+  if (threadIdx.x == 0) count = 0;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) mx = fmaxf(mx, f[i]);
+  // groups of four neighbouring lanes
+  float gm = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
+  if ((lane & 3) == 0) group_max[threadIdx.x >> 2] = orderable(gm);
+  float wm = gm;
+#pragma unroll
+  for (int mask = 4; mask <= 16; mask <<= 1)
+    wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, mask));
+  __syncthreads();
+  if (warp == 0) {
+    // the select-th largest of the groups' maxima: the largest value with at least
+    // `select` maxima at or above it
+    const uint32_t a = group_max[lane], b = group_max[lane + 32];
+    int ra = 0, rb = 0;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const uint32_t v = group_max[i];
+      ra += v >= a;
+      rb += v >= b;
+    }
+    uint32_t best = max(ra >= select ? a : 0u, rb >= select ? b : 0u);
+    best = __reduce_max_sync(0xffffffffu, best);
+    if (lane == 0) threshold = best;
+  }
+  // sum of exponentials relative to the warp's maximum; a NaN makes it NaN
+  const float ref = wm == -INFINITY ? 0.f : wm;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) sum += __expf(f[i] - ref);
+#pragma unroll
+  for (int mask = 1; mask <= 16; mask <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mask);
+  if (lane == 0) {
+    warp_max[warp] = wm;
+    warp_sum[warp] = sum;
+  }
+  __syncthreads();
+  const float lowest = from_orderable(threshold);
+  if (mx >= lowest) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (f[i] >= lowest && f[i] > -INFINITY) {
+        const int at = atomicAdd(&count, 1);
+        if (at < kTileCap)
+          cand[at] = make_key(f[i], base + ((i / EPL) * kBeamThreads + threadIdx.x) * EPL + i % EPL);
+      }
+    }
+  }
+  const size_t out = (size_t)row * tiles + tile;
+  if (threadIdx.x == 0) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, warp_max[w]);
+    float S = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      S += warp_sum[w] * (warp_max[w] == -INFINITY ? 1.f : __expf(warp_max[w] - M));
+    tile_max[out] = M;
+    tile_sum[out] = S;
+  }
+  __syncthreads();
+  uint64_t* keys = tile_keys + out * select;
+  const int n = count;
+  if (n <= kTileCap) {
+    for (int i = threadIdx.x; i < n; i += kBeamThreads) {
+      const uint64_t k = cand[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += cand[j] > k;
+      if (rank < select) keys[rank] = k;
+    }
+    for (int i = n + threadIdx.x; i < select; i += kBeamThreads) keys[i] = 0;
+    return;
+  }
+  // more ties than the buffer holds: one at a time, each the largest below the last
+  uint64_t last = ~0ull;
+  uint64_t* best = cand;  // [kWarps]
+  for (int r = 0; r < select; ++r) {
+    uint64_t k = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const uint64_t c =
+          make_key(f[i], base + ((i / EPL) * kBeamThreads + threadIdx.x) * EPL + i % EPL);
+      if (f[i] > -INFINITY && c < last && c > k) k = c;
+    }
+#pragma unroll
+    for (int mask = 16; mask > 0; mask >>= 1) {
+      const uint64_t o = __shfl_xor_sync(0xffffffffu, k, mask);
+      k = o > k ? o : k;
+    }
+    __syncthreads();
+    if (lane == 0) best[warp] = k;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) k = best[w] > k ? best[w] : k;
+    if (threadIdx.x == 0) keys[r] = k;
+    last = k;
+  }
+}
+
+// Larger is better, ties to the smaller flat index.
+struct Cand {
+  double score;
+  int64_t flat;
+};
+__device__ __forceinline__ bool before(double s, int64_t f, double t, int64_t g) {
+  return s > t || (s == t && f < g);
+}
+
+// One sequence: its rows' logsumexp, then its best `select` candidates.
+__global__ void __launch_bounds__(kMergeThreads)
+    beam_merge_kernel(const float* __restrict__ beam_scores, int beams, int vocab, int select,
+                      int tiles, const float* __restrict__ tile_max,
+                      const float* __restrict__ tile_sum, const uint64_t* __restrict__ tile_keys,
+                      float* __restrict__ scores, int32_t* __restrict__ parents,
+                      int32_t* __restrict__ tokens, int* dev_error) {
+  grid_dependency_wait();
+  allow_dependents();
+  constexpr int kWarps = kMergeThreads / 32;
+  __shared__ double offset[PA_BEAM_MAX];  // beam score less logsumexp, -inf for a dead beam
+  __shared__ double cs[kMergeCap];
+  __shared__ int64_t cf[kMergeCap];
+  __shared__ double maxima[kMergeThreads];
+  __shared__ double threshold;
+  __shared__ int count;
+  const int b = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int k = warp; k < beams; k += kWarps) {
+    const size_t row = (size_t)b * beams + k;
+    float M = -INFINITY;
+    for (int t = lane; t < tiles; t += 32) M = fmaxf(M, tile_max[row * tiles + t]);
+#pragma unroll
+    for (int mask = 16; mask > 0; mask >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, mask));
+    double S = 0.0;
+    for (int t = lane; t < tiles; t += 32) {
+      const float m = tile_max[row * tiles + t], s = tile_sum[row * tiles + t];
+      if (m > -INFINITY || s != s) S += (double)s * exp((double)m - (double)M);
+    }
+#pragma unroll
+    for (int mask = 16; mask > 0; mask >>= 1) S += __shfl_xor_sync(0xffffffffu, S, mask);
+    if (lane == 0) {
+      const float beam = beam_scores[row];
+      double o = -INFINITY;
+      if (M > -INFINITY || S != S) o = (double)beam - ((double)M + log(S));
+      if (o != o || o == INFINITY) {  // a NaN or +inf among the logits, or as beam score
+        report(dev_error, PA_DEVERR_LOGITS);
+        o = -INFINITY;
+      }
+      offset[k] = o;
+    }
+  }
+  if (threadIdx.x == 0) count = 0;
+  __syncthreads();
+  const int per_beam = tiles * select;
+  const int total = beams * per_beam;
+  auto score_of = [&](int i, double& s, int64_t& f) {
+    const int k = i / per_beam;
+    const uint64_t key = tile_keys[(size_t)b * total + i];
+    s = -INFINITY;
+    f = INT64_MAX;
+    if (key != 0 && offset[k] > -INFINITY) {
+      s = offset[k] + (double)from_orderable((uint32_t)(key >> 32));
+      f = (int64_t)k * vocab + (uint32_t)~(uint32_t)key;
+    }
+  };
+  double lowest = -INFINITY;
+  if (total > kMergeCap) {
+    // the select-th largest of the threads' maxima bounds the result from below
+    double m = -INFINITY;
+    for (int i = threadIdx.x; i < total; i += kMergeThreads) {
+      double s;
+      int64_t f;
+      score_of(i, s, f);
+      m = fmax(m, s);
+    }
+    maxima[threadIdx.x] = m;
+    if (threadIdx.x == 0) threshold = -INFINITY;
+    __syncthreads();
+    int at_least = 0, above = 0;
+    for (int j = 0; j < kMergeThreads; ++j) {
+      at_least += maxima[j] >= m;
+      above += maxima[j] > m;
+    }
+    if (at_least >= select && above < select) threshold = m;  // one value
+    __syncthreads();
+    lowest = threshold;
+  }
+  for (int i = threadIdx.x; i < total; i += kMergeThreads) {
+    double s;
+    int64_t f;
+    score_of(i, s, f);
+    if (s > -INFINITY && s >= lowest) {
+      const int at = atomicAdd(&count, 1);
+      if (at < kMergeCap) {
+        cs[at] = s;
+        cf[at] = f;
+      }
+    }
+  }
+  __syncthreads();
+  const int n = count;
+  const size_t out = (size_t)b * select;
+  auto put = [&](int rank, double s, int64_t f) {
+    scores[out + rank] = (float)s;
+    parents[out + rank] = s > -INFINITY ? (int32_t)(f / vocab) : -1;
+    tokens[out + rank] = s > -INFINITY ? (int32_t)(f % vocab) : -1;
+  };
+  if (n <= kMergeCap) {
+    for (int i = threadIdx.x; i < n; i += kMergeThreads) {
+      const double s = cs[i];
+      const int64_t f = cf[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += before(cs[j], cf[j], s, f);
+      if (rank < select) put(rank, s, f);
+    }
+    for (int i = n + threadIdx.x; i < select; i += kMergeThreads) put(i, -INFINITY, 0);
+    return;
+  }
+  // more equal candidates than the buffer holds: one at a time
+  __shared__ double bs[kWarps];
+  __shared__ int64_t bf[kWarps];
+  double ls = INFINITY;
+  int64_t lf = -1;
+  for (int r = 0; r < select; ++r) {
+    double s = -INFINITY;
+    int64_t f = INT64_MAX;
+    for (int i = threadIdx.x; i < total; i += kMergeThreads) {
+      double t;
+      int64_t g;
+      score_of(i, t, g);
+      if (t > -INFINITY && before(ls, lf, t, g) && before(t, g, s, f)) {
+        s = t;
+        f = g;
+      }
+    }
+#pragma unroll
+    for (int mask = 16; mask > 0; mask >>= 1) {
+      const double t = __shfl_xor_sync(0xffffffffu, s, mask);
+      const int64_t g = __shfl_xor_sync(0xffffffffu, f, mask);
+      if (before(t, g, s, f)) {
+        s = t;
+        f = g;
+      }
+    }
+    __syncthreads();
+    if (lane == 0) {
+      bs[warp] = s;
+      bf[warp] = f;
+    }
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w)
+      if (before(bs[w], bf[w], s, f)) {
+        s = bs[w];
+        f = bf[w];
+      }
+    if (threadIdx.x == 0) put(r, s, f);
+    ls = s;
+    lf = f;
+  }
+}
+
+// Elements of a tile: 64 per thread (16-bit) or 32 (fp32) for large work, a
+// quarter for little.
+template <typename T>
+constexpr int tile_elems(bool large) {
+  return kBeamThreads * Logits<T>::kPerLoad * (large ? 8 : 2);
+}
+
+bool large_tiles(int64_t rows, int vocab, int elem) {
+  // enough large tiles for every SM to hold two CTAs
+  const int64_t big = elem == 4 ? tile_elems<float>(true) : tile_elems<__half>(true);
+  return rows * ((vocab + big - 1) / big) >= 148 * 2;
+}
+
+}  // namespace
+
+void beam_layout(int num_seqs, int num_beams, int vocab, int select, int dtype, BeamLayout* lay) {
+  const int elem = dtype == PA_F32 ? 4 : 2;
+  const int64_t rows = (int64_t)num_seqs * num_beams;
+  const bool large = large_tiles(rows, vocab, elem);
+  const int64_t per = elem == 4 ? tile_elems<float>(large) : tile_elems<__half>(large);
+  lay->large = large;
+  lay->tiles = (int)((vocab + per - 1) / per);
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t n = (size_t)rows * lay->tiles;
+  lay->max_off = 0;
+  lay->sum_off = up(n * sizeof(float));
+  lay->key_off = lay->sum_off + up(n * sizeof(float));
+  lay->bytes = lay->key_off + up(n * select * sizeof(uint64_t));
+}
+
+cudaError_t launch_beam_select(const BeamArgs& a, int dtype, cudaStream_t stream) {
+  BeamLayout lay;
+  beam_layout(a.num_seqs, a.num_beams, a.vocab, a.select, dtype, &lay);
+  unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+  float* tm = reinterpret_cast<float*>(ws + lay.max_off);
+  float* ts = reinterpret_cast<float*>(ws + lay.sum_off);
+  uint64_t* tk = reinterpret_cast<uint64_t*>(ws + lay.key_off);
+  const dim3 grid(lay.tiles, a.num_seqs * a.num_beams);
+  auto go = [&](auto kern, auto* x) {
+    return launch_dependent(kern, grid, dim3(kBeamThreads), 0, stream, x, a.row_stride, a.vocab,
+                            a.select, lay.tiles, tm, ts, tk);
+  };
+  cudaError_t e;
+  if (dtype == PA_F32) {
+    auto* x = static_cast<const float*>(a.logits);
+    e = lay.large ? go(beam_tile_kernel<float, 8>, x) : go(beam_tile_kernel<float, 2>, x);
+  } else if (dtype == PA_F16) {
+    auto* x = static_cast<const __half*>(a.logits);
+    e = lay.large ? go(beam_tile_kernel<__half, 8>, x) : go(beam_tile_kernel<__half, 2>, x);
+  } else {
+    auto* x = static_cast<const __nv_bfloat16*>(a.logits);
+    e = lay.large ? go(beam_tile_kernel<__nv_bfloat16, 8>, x)
+                  : go(beam_tile_kernel<__nv_bfloat16, 2>, x);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_dependent(beam_merge_kernel, dim3(a.num_seqs), dim3(kMergeThreads), 0, stream,
+                          a.beam_scores, a.num_beams, a.vocab, a.select, lay.tiles,
+                          (const float*)tm, (const float*)ts, (const uint64_t*)tk, a.scores,
+                          a.parents, a.tokens, a.dev_error);
+}
+
+}  // namespace pa

@@ -10,59 +10,18 @@
 
 namespace pa {
 
-// Outputs are multiplied by a.out_scale (the value scale of an E4M3 cache, else 1).
-// After the main loop every warp w has left, in shared memory,
-//   red_m[w][g], red_l[w][g]   its running max (base 2) and sum of exponentials
-//   red_acc[w][g][D]           its unnormalised output rows
-// for the G query heads of this CTA's KV head. This merges them by rescaling
-// to the common maximum. A sequence with a single partition writes `out`
-// directly. Otherwise the CTA stores its partition state in the workspace, and
-// the CTA that completes the sequence's last partition merges all partitions
-// in logical order and returns the counter to zero. With a.states_only every
-// partition stores its state and nothing is merged.
-// `wts` (>= nparts * G floats of shared memory) may alias red_*: it is written
-// only after they have been read. Every thread of the CTA must call this with
-// the same arguments; it ends with a barrier, so shared memory it used can be
-// rewritten as soon as it returns.
+// The split-KV merge in the same launch: called by every thread of a CTA that has
+// stored its partition's state in the workspace. The CTA that completes the
+// sequence's last partition merges all of them in logical order, writes the
+// output rows (times a.out_scale) and returns the counter to zero. `wts`:
+// >= nparts * G floats of shared memory that no thread reads any more. It ends
+// with a barrier.
 template <typename T, int D, int G, int WARPS>
-__device__ __forceinline__ void finish_partition(const DecodeArgs& a, float* wts,
-                                                 const float* red_m, const float* red_l,
-                                                 const float* red_acc, int s, int kvh, int part,
-                                                 int nparts, T* out_rows) {
+__device__ __forceinline__ void merge_if_last(const DecodeArgs& a, float* wts, int s, int kvh,
+                                              int nparts, T* out_rows) {
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const bool split = nparts > 1 || a.states_only;
   const size_t unit = (size_t)s * a.num_kv_heads + kvh;
-  for (int item = threadIdx.x; item < G * D; item += blockDim.x) {
-    const int g = item / D;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, red_m[w * G + g]);
-    // M is finite unless every block of the partition was skipped as out of range
-    const float Mref = M == -INFINITY ? 0.f : M;
-    float L = 0.f, A = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float sc = exp2f(red_m[w * G + g] - Mref);
-      L = fmaf(sc, red_l[w * G + g], L);
-      A = fmaf(sc, red_acc[(w * G) * D + item], A);
-    }
-    if (!split) {
-      out_rows[item] = Storage<T>::from_f32(L > 0.f ? (A / L) * a.out_scale : 0.f);
-    } else {
-      const size_t row = (unit * a.max_parts + part) * G + g;
-      a.ws_acc[row * D + (item % D)] = A;
-      if (item % D == 0) {
-        a.ws_m[row] = M;
-        a.ws_l[row] = L;
-      }
-    }
-  }
-  if (!split || a.states_only) {
-    __syncthreads();
-    return;
-  }
-
   // ---- split-KV: the last partition to finish merges all of them.
   // The barrier makes every thread's partial-result stores visible to thread 0,
   // whose gpu-scope acq_rel add then publishes them (release is cumulative) and,
@@ -160,6 +119,59 @@ __device__ __forceinline__ void finish_partition(const DecodeArgs& a, float* wts
   }
   if (threadIdx.x == 0) a.ws_count[unit] = 0;
   __syncthreads();
+}
+
+// Outputs are multiplied by a.out_scale (the value scale of an E4M3 cache, else 1).
+// After the main loop every warp w has left, in shared memory,
+//   red_m[w][g], red_l[w][g]   its running max (base 2) and sum of exponentials
+//   red_acc[w][g][D]           its unnormalised output rows
+// for the G query heads of this CTA's KV head. This merges them by rescaling
+// to the common maximum. A sequence with a single partition writes `out`
+// directly. Otherwise the CTA stores its partition state in the workspace, and
+// the CTA that completes the sequence's last partition merges all partitions
+// in logical order and returns the counter to zero. With a.states_only every
+// partition stores its state and nothing is merged.
+// `wts` (>= nparts * G floats of shared memory) may alias red_*: it is written
+// only after they have been read. Every thread of the CTA must call this with
+// the same arguments; it ends with a barrier, so shared memory it used can be
+// rewritten as soon as it returns.
+template <typename T, int D, int G, int WARPS>
+__device__ __forceinline__ void finish_partition(const DecodeArgs& a, float* wts,
+                                                 const float* red_m, const float* red_l,
+                                                 const float* red_acc, int s, int kvh, int part,
+                                                 int nparts, T* out_rows) {
+  const bool split = nparts > 1 || a.states_only;
+  const size_t unit = (size_t)s * a.num_kv_heads + kvh;
+  for (int item = threadIdx.x; item < G * D; item += blockDim.x) {
+    const int g = item / D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, red_m[w * G + g]);
+    // M is finite unless every block of the partition was skipped as out of range
+    const float Mref = M == -INFINITY ? 0.f : M;
+    float L = 0.f, A = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float sc = exp2f(red_m[w * G + g] - Mref);
+      L = fmaf(sc, red_l[w * G + g], L);
+      A = fmaf(sc, red_acc[(w * G) * D + item], A);
+    }
+    if (!split) {
+      out_rows[item] = Storage<T>::from_f32(L > 0.f ? (A / L) * a.out_scale : 0.f);
+    } else {
+      const size_t row = (unit * a.max_parts + part) * G + g;
+      a.ws_acc[row * D + (item % D)] = A;
+      if (item % D == 0) {
+        a.ws_m[row] = M;
+        a.ws_l[row] = L;
+      }
+    }
+  }
+  if (!split || a.states_only) {
+    __syncthreads();
+    return;
+  }
+  merge_if_last<T, D, G, WARPS>(a, wts, s, kvh, nparts, out_rows);
 }
 
 // The warp-per-partition split's counterpart: merges the warps' states (WARPS

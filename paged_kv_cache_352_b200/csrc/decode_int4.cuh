@@ -74,15 +74,27 @@ constexpr int kInt4Warps = 4;
 constexpr int kInt4Stages = 3;
 constexpr int kInt4CtasPerSm = 4;  // 128 registers a thread
 
-// Copies BYTES (8 or 16) from global to shared memory asynchronously.
-template <int BYTES>
-__device__ __forceinline__ void cp_async(void* smem, const void* gmem) {
+// Copies BYTES (8 or 16) from global to shared memory (a 32-bit shared address)
+// asynchronously.
+template <int BYTES, int DST_OFF = 0, int SRC_OFF = 0>
+__device__ __forceinline__ void cp_async(uint32_t smem, const void* gmem) {
   if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(gmem)
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(smem), "l"(gmem),
+                 "n"(DST_OFF), "n"(SRC_OFF)
                  : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(smem)), "l"(gmem)
+    asm volatile("cp.async.ca.shared.global [%0 + %2], [%1 + %3], 8;" ::"r"(smem), "l"(gmem),
+                 "n"(DST_OFF), "n"(SRC_OFF)
                  : "memory");
+}
+// A lane's four chunks of a block's codes: two of K, two of V.
+template <int CB>
+__device__ __forceinline__ void copy_block(uint32_t dst, const unsigned char* k,
+                                           const unsigned char* v) {
+  cp_async<CB>(dst, k);
+  cp_async<CB, 32 * CB, 32 * CB>(dst, k);
+  cp_async<CB, 64 * CB>(dst, v);
+  cp_async<CB, 96 * CB, 32 * CB>(dst, v);
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -124,6 +136,30 @@ __device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&w)
   }
 }
 
+// Largest magnitude of eight 16-bit elements.
+template <typename T>
+struct Amax;
+template <>
+struct Amax<__half> {
+  static __device__ __forceinline__ float of(const uint4& u) {
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
+    const __half2 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])),
+                              __hmax2(__habs2(h[2]), __habs2(h[3])));
+    const float2 f = __half22float2(m);
+    return fmaxf(f.x, f.y);
+  }
+};
+template <>
+struct Amax<__nv_bfloat16> {
+  static __device__ __forceinline__ float of(const uint4& u) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])),
+                                     __hmax2(__habs2(h[2]), __habs2(h[3])));
+    const float2 f = __bfloat1622float2(m);
+    return fmaxf(f.x, f.y);
+  }
+};
+
 // One warp's running softmax state over 4-bit tiles.
 template <typename T, int D, int G>
 struct Int4State {
@@ -139,9 +175,12 @@ struct Int4State {
   int g, c, lane;
   uint4 qraw[W];
   uint32_t qb[KSTEPS][2];           // head g's operand
-  // of heads 2c, 2c + 1; l and pmid are this lane's share (tokens g, g + 8)
-  float m[2], l[2], pmid[2], row_scale[2], qsum[2];
-  float vmax, vinv;                 // S and 2^7 / S (both 0 until a positive scale comes)
+  // Of heads 2c, 2c + 1. Everything accumulated is in units of 2^ref: ref is the
+  // softmax reference m plus log2 S - 7, S a power of two at or above every value
+  // scale seen (0 before the first positive one). l and pmid are this lane's share
+  // (tokens g, g + 8).
+  float m[2], ref[2], l[2], pmid[2], row_scale[2], qsum[2];
+  float vmax;  // S
   float o[MT][4], ow[4];
 
   // the head of column h
@@ -161,20 +200,17 @@ struct Int4State {
   __device__ __forceinline__ void begin(float scale_log2) {
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      float f[8];
-      Storage<T>::to_f32(qraw[i], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-    }
+    for (int i = 0; i < W; ++i) amax = fmaxf(amax, Amax<T>::of(qraw[i]));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     // 2^-k brings the row's largest element to [2^14, 2^15)
     int k = amax > 0.f && amax < INFINITY ? ilogbf(amax) - 14 : 0;
     if (k < -100) k = -100;
     const float down = exp2f((float)-k);
-    const float rs = scale_log2 * exp2f((float)k);
-    float qs = 0.f;
+    // The products are in units of 2^-24. The cap keeps the factor finite for rows
+    // past 2^117, whose scores lie more than 2^50 apart with or without it.
+    const float rs = scale_log2 * exp2f((float)(k + 24 < 125 ? k + 24 : 125));
+    float qs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       float f[8];
@@ -184,23 +220,23 @@ struct Int4State {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {  // low nibbles: dimensions 2r, 2r + 4; high: one more
         const __half2 lo = __floats2half2_rn(f[2 * r], f[2 * r + 4]);
-        const __half2 hi = __floats2half2_rn(f[2 * r + 1] * 0.0625f, f[2 * r + 5] * 0.0625f);
-        const float2 fl = __half22float2(lo), fh = __half22float2(hi);
-        qs += (fl.x + fl.y) + 16.f * (fh.x + fh.y);
+        const __half2 hi = __hmul2(__floats2half2_rn(f[2 * r + 1], f[2 * r + 5]),
+                                   __float2half2_rn(0.0625f));
         memcpy(&qb[2 * j + r][0], &lo, 4);
         memcpy(&qb[2 * j + r][1], &hi, 4);
+        // sum q as the product with codes of 1, in the layout of the scores
+        mma_16816(qs, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qb[2 * j + r][0],
+                  qb[2 * j + r][1]);
       }
     }
-    qs += __shfl_xor_sync(0xffffffffu, qs, 1);
-    qs += __shfl_xor_sync(0xffffffffu, qs, 2);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      qsum[e] = __shfl_sync(0xffffffffu, qs, 8 * c + 4 * e);
+      qsum[e] = qs[e];
       row_scale[e] = __shfl_sync(0xffffffffu, rs, 8 * c + 4 * e);
       m[e] = -INFINITY;
-      l[e] = pmid[e] = 0.f;
+      ref[e] = l[e] = pmid[e] = 0.f;
     }
-    vmax = vinv = 0.f;
+    vmax = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       ow[e] = 0.f;
@@ -214,6 +250,37 @@ struct Int4State {
     return half2_bits_to_float2(*reinterpret_cast<const uint32_t*>(p + 4 * t));
   }
 
+  // A softmax reference or the value-scale reference S moves: brings what has
+  // accumulated to the new ones (which are the same in every lane of a column).
+  __device__ __forceinline__ void move(float (&bmax)[2], float smax) {
+#pragma unroll
+    for (int mask = 4; mask <= 16; mask <<= 1) {
+      bmax[0] = fmaxf(bmax[0], __shfl_xor_sync(0xffffffffu, bmax[0], mask));
+      bmax[1] = fmaxf(bmax[1], __shfl_xor_sync(0xffffffffu, bmax[1], mask));
+      smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, mask));
+    }
+    // the power of two at or above smax (a half: exact here)
+    if (smax > vmax)
+      vmax = __uint_as_float((__float_as_uint(smax) + 0x007fffffu) & 0x7f800000u);
+    const float shift = vmax > 0.f ? (float)((int)(__float_as_uint(vmax) >> 23) - 127 - 7) : 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const bool first = m[e] == -INFINITY;  // nothing of this head has accumulated
+      if (bmax[e] > m[e] + kLazyRescaleLog2) m[e] = bmax[e];
+      const float to = (m[e] == -INFINITY ? 0.f : m[e]) + shift;
+      const float alpha = first ? 1.f : exp2f(ref[e] - to);
+      ref[e] = to;
+      l[e] *= alpha;
+      pmid[e] *= alpha;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        o[t][e] *= alpha;
+        o[t][2 + e] *= alpha;
+      }
+      ow[e] *= alpha;
+    }
+  }
+
   // Two blocks, `codes` and `par` as Int4Stage lays them out. kMask: block i has
   // valid<i> tokens inside the context (0: not copied); what lies in the others'
   // slots may be any bits.
@@ -225,7 +292,8 @@ struct Int4State {
     float x[2][4];  // [block][2 i + e]: token g + 8 i, head 2c + e
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.f;
+      x[b][0] = x[b][2] = -7.5f * qsum[0];  // the product starts from the codes' centre
+      x[b][1] = x[b][3] = -7.5f * qsum[1];
       const unsigned char* kc = codes + b * 2 * kCodeBytes + lane * (4 * W);
       uint32_t ka[W], kb[W];
       load_words<W>(kc, ka);
@@ -253,61 +321,27 @@ struct Int4State {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float& y = x[b][2 * i + e];
-          const float dot = fmaf(y, 16777216.f, -7.5f * qsum[e]);
-          y = fmaf(kp.x, dot, kp.y * qsum[e]) * row_scale[e];
+          y = fmaf(kp.x, y, kp.y * qsum[e]) * row_scale[e];
           if (!in(b, i)) y = -INFINITY;
           bmax[e] = fmaxf(bmax[e], y);
         }
       }
     const bool moved =
         bmax[0] > m[0] + kLazyRescaleLog2 || bmax[1] > m[1] + kLazyRescaleLog2 || smax > vmax;
-    if (__any_sync(0xffffffffu, moved)) {
-      // a softmax reference or the value-scale reference S moves: bring the sums
-      // to the new ones (the same in every lane of a column)
-#pragma unroll
-      for (int mask = 4; mask <= 16; mask <<= 1) {
-        bmax[0] = fmaxf(bmax[0], __shfl_xor_sync(0xffffffffu, bmax[0], mask));
-        bmax[1] = fmaxf(bmax[1], __shfl_xor_sync(0xffffffffu, bmax[1], mask));
-        smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, mask));
-      }
-      float f = 1.f;
-      if (smax > vmax) {
-        // the power of two at or above smax (a half: exact here)
-        const float s2 = __uint_as_float((__float_as_uint(smax) + 0x007fffffu) & 0x7f800000u);
-        f = vmax / s2;
-        vmax = s2;
-        vinv = 128.f / s2;
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float alpha;
-        lazy_reference(m[e], bmax[e], alpha);
-        l[e] *= alpha;
-        pmid[e] *= alpha;
-        alpha *= f;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          o[t][e] *= alpha;
-          o[t][2 + e] *= alpha;
-        }
-        ow[e] *= alpha;
-      }
-    }
-    const float mref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    if (__any_sync(0xffffffffu, moved)) move(bmax, smax);
     // ---- O^T += V^T P^T
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       uint32_t pb[2], lo[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float sv = vp[b][i].x * vinv;
         float w[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float p = fast_exp2(x[b][2 * i + e] - mref[e]);
+          const float p = fast_exp2(x[b][2 * i + e] - ref[e]);
           l[e] += p;
           pmid[e] = fmaf(p, vp[b][i].y, pmid[e]);
-          w[e] = p * sv;  // at most 2^8 2^7 (the reference is lazy by 2^8)
+          w[e] = p * vp[b][i].x;  // at most 2^8 2^7: m is lazy by 2^8, and S >= the scale
         }
         const __half2 h = __floats2half2_rn(w[0], w[1]);
         memcpy(&pb[i], &h, 4);
@@ -341,7 +375,9 @@ struct Int4State {
     }
   }
 
-  __device__ __forceinline__ void to_red(float* red_m, float* red_l, float* red_acc, int warp) {
+  // Sums the shares of the lanes: l and pmid over the tokens, the residual's
+  // columns into the heads'.
+  __device__ __forceinline__ void close() {
     if constexpr (kRepeat) {  // columns 4-7 hold the residual's share of heads 0-3
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -350,27 +386,23 @@ struct Int4State {
         ow[e] += __shfl_xor_sync(0xffffffffu, ow[e], 2);
       }
     }
-    const float back = vmax * 0.0078125f;  // 1 / vinv
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int mask = 4; mask <= 16; mask <<= 1) {
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], mask);
         pmid[e] += __shfl_xor_sync(0xffffffffu, pmid[e], mask);
       }
-      const int h = 2 * c + e;
-      if (h < G) {
-        if (g == 0) {
-          red_m[warp * G + h] = m[e];
-          red_l[warp * G + h] = l[e];
-        }
-        float2* dst = reinterpret_cast<float2*>(red_acc + (warp * G + h) * D + 4 * W * g);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          dst[t] = make_float2(fmaf(fmaf(o[t][e], 16777216.f, -7.5f * ow[e]), back, pmid[e]),
-                               fmaf(fmaf(o[t][2 + e], 1048576.f, -7.5f * ow[e]), back, pmid[e]));
-      }
-    }
+  }
+
+  // Unnormalised outputs (in units of 2^ref) of head 2c + e: dimensions
+  // 4W g + 4q .. + 3.
+  __device__ __forceinline__ float4 row4(int e, int q) const {
+    const float base = fmaf(-7.5f, ow[e], pmid[e]);
+    return make_float4(fmaf(o[2 * q][e], 16777216.f, base),
+                       fmaf(o[2 * q][2 + e], 1048576.f, base),
+                       fmaf(o[2 * q + 1][e], 16777216.f, base),
+                       fmaf(o[2 * q + 1][2 + e], 1048576.f, base));
   }
 };
 
@@ -410,13 +442,15 @@ __global__ void __launch_bounds__(kInt4Warps * 32, kInt4CtasPerSm)
   const int first = part * a.part_blocks + (a.warp_parts ? 0 : 2 * warp);
   const int stride = a.warp_parts ? 2 : 2 * WARPS;
   const int32_t* table = a.block_tables + (size_t)s * a.max_blocks_per_seq;
+  // Independent loads first, so that their latencies overlap: the context length,
+  // the first 32 table entries of the warp (lane i: block i & 1 of pair i / 2;
+  // entries past the sequence are padding, never used) and q.
   int ctx = __ldg(a.context_lens + s);
-  // lane i holds the table entry of block i & 1 of pair base + i / 2
-  auto entries = [&](int base) {
-    const long long b = first + (long long)(base + (lane >> 1)) * stride + (lane & 1);
-    return b < a.max_blocks_per_seq ? __ldg(table + b) : -1;
-  };
-  int win = entries(0);
+  int raw_entry = -1;
+  {
+    const long long b = first + (long long)(lane >> 1) * stride + (lane & 1);
+    if (b < a.max_blocks_per_seq) raw_entry = __ldg(table + b);
+  }
   St st;
   st.prefetch_q(a, s, kvh, lane);
   if (ctx < 0 || ctx > a.max_blocks_per_seq * kBlockSize || ctx > a.max_context_len) {
@@ -436,53 +470,62 @@ __global__ void __launch_bounds__(kInt4Warps * 32, kInt4CtasPerSm)
   const int last = min(nblk, (part + 1) * a.part_blocks);  // blocks end here
   const int pairs = last > first ? (last - first + stride - 1) / stride : 0;
 
-  unsigned char* ring = smem + (size_t)warp * STAGES * Stage::kBytes;
-  const uint32_t block_stride = (uint32_t)a.num_kv_heads * St::kTileBytes;
-  const unsigned char* kt = static_cast<const unsigned char*>(a.k_cache) +
-                            (size_t)kvh * St::kTileBytes;
-  const unsigned char* vt = static_cast<const unsigned char*>(a.v_cache) +
-                            (size_t)kvh * St::kTileBytes;
-  // lanes 0-15 copy the parameters: 16 bytes (lane & 3) of K or V (lane & 4) of block lane / 8
-  const unsigned char* par_src = ((lane & 4) ? vt : kt) + St::kCodeBytes + 16 * (lane & 3);
-  const int par_dst = Stage::kParOff + 16 * (lane & 15);
+  // Entry of the table as the place of its tile: offset / 64 (tiles are multiples
+  // of 64 bytes; 2^38 bytes of pool), kNone past the warp's blocks, kBad outside
+  // the pool. Lane i holds block i & 1 of pair base + i / 2.
+  constexpr uint32_t kNone = 0xfffffffeu, kBad = 0xffffffffu;
+  static_assert(St::kTileBytes % 64 == 0, "tile places are counted in 64 bytes");
+  const uint32_t block_units = (uint32_t)a.num_kv_heads * (St::kTileBytes / 64);
+  auto in_range = [&](int base) {
+    const int pair = base + (lane >> 1);
+    return pair < pairs && first + pair * stride + (lane & 1) < last;
+  };
+  auto place = [&](int e) -> uint32_t {
+    return (unsigned)e < (unsigned)a.num_blocks ? (uint32_t)e * block_units : kBad;
+  };
+  auto entries = [&](int base) -> uint32_t {
+    return in_range(base) ? place(__ldg(table + first + (base + (lane >> 1)) * stride + (lane & 1)))
+                          : kNone;
+  };
+  uint32_t win = in_range(0) ? place(raw_entry) : kNone;
+  uint32_t win_next = entries(16);
 
-  int win_next = pairs > 16 ? entries(16) : -1;
-  uint32_t copied = 0;  // bits 2 st, 2 st + 1: blocks 0 and 1 of stage st were copied
+  // shared-memory places of this lane's chunks in stage 0, and their sources less
+  // the tile's offset; lanes 0-15 copy the parameters: 16 bytes (lane & 3) of K or V
+  // (lane & 4) of block lane / 8
+  const uint32_t ring = smem_addr(smem) + warp * STAGES * Stage::kBytes;
+  const unsigned char* kt = static_cast<const unsigned char*>(a.k_cache) +
+                            (size_t)kvh * St::kTileBytes + lane * CB;
+  const unsigned char* vt = static_cast<const unsigned char*>(a.v_cache) +
+                            (size_t)kvh * St::kTileBytes + lane * CB;
+  const unsigned char* par_src = ((lane & 4) ? vt : kt) - lane * CB + St::kCodeBytes +
+                                 16 * (lane & 3);
+  const uint32_t par_dst = Stage::kParOff + 16 * (lane & 15);
+  uint32_t skipped = 0;  // bits 2 st, 2 st + 1: block 0 or 1 of stage st was not copied
   auto issue = [&](int jp, int stg) {
     if (jp < pairs) {
       if ((jp & 15) == 0 && jp > 0) {
         win = win_next;
-        win_next = jp + 16 < pairs ? entries(jp + 16) : -1;
+        win_next = entries(jp + 16);
       }
-      const int b0 = first + jp * stride;
-      const int e0 = __shfl_sync(0xffffffffu, win, 2 * (jp & 15));
-      const int e1 = __shfl_sync(0xffffffffu, win, 2 * (jp & 15) + 1);
-      const bool ok0 = (unsigned)e0 < (unsigned)a.num_blocks;
-      const bool has1 = b0 + 1 < last;
-      const bool ok1 = has1 && (unsigned)e1 < (unsigned)a.num_blocks;
-      copied = (copied & ~(3u << (2 * stg))) | ((ok0 ? 1u : 0u) | (ok1 ? 2u : 0u)) << (2 * stg);
-      if (!ok0 || (has1 && !ok1)) {
-        if (lane == 0) report(a.dev_error, PA_DEVERR_BLOCK_RANGE);
+      const uint32_t e0 = __shfl_sync(0xffffffffu, win, 2 * (jp & 15));
+      const uint32_t e1 = __shfl_sync(0xffffffffu, win, 2 * (jp & 15) + 1);
+      const uint32_t dst = ring + stg * Stage::kBytes;
+      const uint64_t off0 = (uint64_t)e0 * 64u, off1 = (uint64_t)e1 * 64u;
+      if (max(e0, e1) < kNone) {
+        copy_block<CB>(dst + lane * CB, kt + off0, vt + off0);
+        copy_block<CB>(dst + (128 + lane) * CB, kt + off1, vt + off1);
+        if (lane < 16) cp_async<16>(dst + par_dst, par_src + (lane < 8 ? off0 : off1));
+        if (skipped) skipped &= ~(3u << (2 * stg));
+      } else {  // the last block of an odd count, or a bad entry
+        const bool ok0 = e0 < kNone, ok1 = e1 < kNone;
+        if (ok0) copy_block<CB>(dst + lane * CB, kt + off0, vt + off0);
+        if (ok1) copy_block<CB>(dst + (128 + lane) * CB, kt + off1, vt + off1);
+        if (lane < 16 && (lane < 8 ? ok0 : ok1))
+          cp_async<16>(dst + par_dst, par_src + (lane < 8 ? off0 : off1));
+        skipped = (skipped & ~(3u << (2 * stg))) | ((ok0 ? 0u : 1u) | (ok1 ? 0u : 2u)) << (2 * stg);
+        if ((e0 == kBad || e1 == kBad) && lane == 0) report(a.dev_error, PA_DEVERR_BLOCK_RANGE);
       }
-      unsigned char* dst = ring + stg * Stage::kBytes;
-      const uint64_t off0 = (uint64_t)(uint32_t)e0 * block_stride;
-      const uint64_t off1 = (uint64_t)(uint32_t)e1 * block_stride;
-      if (ok0) {
-        unsigned char* to = dst + lane * CB;
-        cp_async<CB>(to, kt + off0 + lane * CB);
-        cp_async<CB>(to + 32 * CB, kt + off0 + (32 + lane) * CB);
-        cp_async<CB>(to + 64 * CB, vt + off0 + lane * CB);
-        cp_async<CB>(to + 96 * CB, vt + off0 + (32 + lane) * CB);
-      }
-      if (ok1) {
-        unsigned char* to = dst + (128 + lane) * CB;
-        cp_async<CB>(to, kt + off1 + lane * CB);
-        cp_async<CB>(to + 32 * CB, kt + off1 + (32 + lane) * CB);
-        cp_async<CB>(to + 64 * CB, vt + off1 + lane * CB);
-        cp_async<CB>(to + 96 * CB, vt + off1 + (32 + lane) * CB);
-      }
-      if (lane < 16 && (lane < 8 ? ok0 : ok1))
-        cp_async<16>(dst + par_dst, par_src + (lane < 8 ? off0 : off1));
     }
     cp_async_commit();  // a group per step, also an empty one: the waits count groups
   };
@@ -490,44 +533,103 @@ __global__ void __launch_bounds__(kInt4Warps * 32, kInt4CtasPerSm)
   st.begin(a.scale_log2);
 
   int stg = 0;
+  const int limit = ctx - first * kBlockSize;  // tokens from the warp's first block on
   for (int j = 0; j < pairs; ++j) {
     cp_async_wait<STAGES - 2>();
     // publishes the parameters that other lanes copied, and orders this step's
     // copies behind every lane's reads of the stage they go to (step j - 1's)
     __syncwarp();
-    const int next = stg == 0 ? STAGES - 1 : stg - 1;
-    issue(j + STAGES - 1, next);
-    const unsigned char* codes = ring + stg * Stage::kBytes;
-    const uint32_t got = (copied >> (2 * stg)) & 3u;
-    const int b0 = first + j * stride;
-    const int v0 = (got & 1u) ? ctx - b0 * kBlockSize : 0;
-    const int v1 = (got & 2u) ? ctx - (b0 + 1) * kBlockSize : 0;
-    if (v0 >= kBlockSize && v1 >= kBlockSize)
-      st.template step<false>(codes, codes + Stage::kParOff, kBlockSize, kBlockSize);
-    else if (got)
-      st.template step<true>(codes, codes + Stage::kParOff, v0, v1);
+    issue(j + STAGES - 1, stg == 0 ? STAGES - 1 : stg - 1);
+    const unsigned char* codes = smem + (warp * STAGES + stg) * Stage::kBytes;
+    const int v0 = limit - j * stride * kBlockSize;
+    const uint32_t miss = (skipped >> (2 * stg)) & 3u;
+    if (v0 >= 2 * kBlockSize && miss == 0)
+      st.template step<false>(codes, codes + Stage::kParOff, 0, 0);
+    else if (miss != 3u)
+      st.template step<true>(codes, codes + Stage::kParOff, (miss & 1u) ? 0 : v0,
+                             (miss & 2u) ? 0 : v0 - kBlockSize);
     stg = stg == STAGES - 1 ? 0 : stg + 1;
   }
   cp_async_wait<0>();
 
+  // ---- merge the warps. Every warp has the same layout of outputs, so each scales
+  // its own to the common reference and leaves them by lane: no bank conflicts, and
+  // the thread that adds up a float4 already holds its heads' sums.
+  st.close();
+  __shared__ float red_m[WARPS][8], red_l[WARPS][8];
+  if (st.g == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      red_m[warp][2 * st.c + e] = st.m[e] == -INFINITY ? -INFINITY : st.ref[e];
+      red_l[warp][2 * st.c + e] = st.l[e];
+    }
+  }
+  __syncthreads();  // (and every warp is done with its ring)
+  constexpr int W = St::W, POS = 2 * W;  // float4 positions of a lane: (e, q)
+  float4* red_acc = reinterpret_cast<float4*>(smem);  // [WARPS][POS][32]
+  float M[2], L[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int h = 2 * st.c + e;
+    M[e] = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M[e] = fmaxf(M[e], red_m[w][h]);
+    // finite unless every block of the partition was skipped as out of range
+    const float mr = M[e] == -INFINITY ? 0.f : M[e];
+    L[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) L[e] = fmaf(exp2f(red_m[w][h] - mr), red_l[w][h], L[e]);
+    const float sc = exp2f(red_m[warp][h] - mr);
+    if (h < G) {
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        const float4 v = st.row4(e, q);
+        red_acc[(warp * POS + e * W + q) * 32 + lane] =
+            make_float4(v.x * sc, v.y * sc, v.z * sc, v.w * sc);
+      }
+    }
+  }
   __syncthreads();
-  float* red_m = reinterpret_cast<float*>(smem);  // [WARPS][G]
-  float* red_l = red_m + WARPS * G;                // [WARPS][G]
-  float* red_acc = red_l + WARPS * G;              // [WARPS][G][D]
-  st.to_red(red_m, red_l, red_acc, warp);
-  __syncthreads();
-  if (a.warp_parts)
-    store_cta_state<D, G, WARPS>(a, red_m, red_l, red_acc, s, kvh, blockIdx.y);
-  else
-    finish_partition<T, D, G, WARPS>(a, red_m, red_m, red_l, red_acc, s, kvh, part, nparts,
-                                     out_rows);
+  const bool split = a.warp_parts || nparts > 1;
+  const size_t row0 = (((size_t)s * a.num_kv_heads + kvh) * a.max_parts + blockIdx.y) * G;
+#pragma unroll
+  for (int i = 0; i < POS / WARPS; ++i) {
+    const int pos = warp * (POS / WARPS) + i;
+    const int e = pos / W, q = pos % W;
+    const int h = 2 * st.c + e;
+    if (h >= G) continue;
+    float4 v = red_acc[pos * 32 + lane];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) {
+      const float4 u = red_acc[(w * POS + pos) * 32 + lane];
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    const int dim = 4 * W * st.g + 4 * q;
+    const float Mh = e ? M[1] : M[0], Lh = e ? L[1] : L[0];
+    if (!split) {
+      const float f = Lh > 0.f || Lh != Lh ? 1.f / Lh : 0.f;
+      T r[4] = {Storage<T>::from_f32(v.x * f), Storage<T>::from_f32(v.y * f),
+                Storage<T>::from_f32(v.z * f), Storage<T>::from_f32(v.w * f)};
+      uint2 packed;
+      memcpy(&packed, r, sizeof(packed));
+      *reinterpret_cast<uint2*>(out_rows + h * D + dim) = packed;
+    } else {
+      *reinterpret_cast<float4*>(a.ws_acc + (row0 + h) * D + dim) = v;
+      if (dim == 0) {
+        a.ws_m[row0 + h] = Mh;
+        a.ws_l[row0 + h] = Lh;
+      }
+    }
+  }
+  if (!split || a.warp_parts) return;
+  merge_if_last<T, D, G, WARPS>(a, reinterpret_cast<float*>(smem), s, kvh, nparts, out_rows);
 }
 
 template <typename T, int D, int G>
 cudaError_t launch_int4(const DecodeArgs& a, cudaStream_t stream) {
   constexpr int WARPS = kInt4Warps;
   const size_t ring = size_t(WARPS) * kInt4Stages * Int4Stage<D>::kBytes;
-  const size_t red = size_t(WARPS) * G * (D + 2) * sizeof(float);
+  const size_t red = size_t(WARPS) * 8 * D * sizeof(float);
   const size_t wts = (size_t)a.max_parts * G * sizeof(float);
   size_t smem = ring > red ? ring : red;
   if (smem < wts) smem = wts;
@@ -545,7 +647,7 @@ cudaError_t launch_int4(const DecodeArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready[dev].store(true, std::memory_order_release);
   }
-  const int y = a.warp_parts ? (a.max_parts + WARPS - 1) / WARPS : a.max_parts;
+  const int y = a.warp_parts == 1 ? (a.max_parts + WARPS - 1) / WARPS : a.max_parts;
   e = launch_dependent(kern, dim3(a.num_kv_heads, y, a.num_seqs), dim3(WARPS * 32), smem, stream,
                        a);
   if (e != cudaSuccess || !a.warp_parts) return e;

@@ -79,7 +79,8 @@ struct DecodeArgs {
   int max_parts;     // partitions per sequence the grid covers
   float scale_log2;  // softmax scale * log2(e) (* the key scale of an E4M3 cache)
   float out_scale;   // 1, or the value scale of an E4M3 cache
-  int warp_parts;    // split mode: one warp per partition + a merge launch (else one CTA)
+  int warp_parts;    // split mode: one warp per partition + a merge launch (else one CTA);
+                     // 2 (4-bit caches): max_parts counts groups of four partitions
   int states_only;   // every partition leaves its state in the workspace; nothing writes
                      // `out` and no partitions are merged (a sequence with no blocks
                      // leaves no state): the caller merges them
