@@ -63,7 +63,13 @@ typedef enum pa_status {
  * pa_swap_blocks move them (one byte per element; head_dim/2 + 4 bytes per token
  * and KV head). Queries, outputs and the 16-bit inputs of the cache writes are
  * PA_F16 or PA_BF16. */
-typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } pa_dtype;
+typedef enum pa_dtype {
+  PA_F16 = 0,
+  PA_BF16 = 1,
+  PA_FP8_E4M3 = 2,
+  PA_INT4 = 3,
+  PA_F32 = 4 /* logits only */
+} pa_dtype;
 
 /* Bits OR-ed into *dev_error by device calls. */
 #define PA_DEVERR_SLOT_RANGE 1    /* slot >= num_blocks * block_size: token not written */
@@ -78,6 +84,8 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2, PA_INT4 = 3 } 
                                      correct */
 #define PA_DEVERR_POSITION 32     /* a token's position outside [0, num_positions): the token
                                      was neither rotated nor written */
+#define PA_DEVERR_LOGITS 64       /* a NaN or +inf among a beam's logits, or as its score: the
+                                     beam gave no candidates */
 
 /* Message for the last failed call on this thread ("" if none). */
 const char* pa_last_error(void);
@@ -342,6 +350,45 @@ int pa_rope_and_cache_int4(void* q_out, const void* q, const void* key, const vo
  * frequencies theta^(-2i / rotary_dim), angles and functions in double
  * precision, rounded to float. */
 int pa_rope_table(float* cos_sin, int num_positions, int rotary_dim, double theta);
+
+/* ---------------------------------------------------------------------------
+ * pa_beam_select — beam search's selection over beams and vocabulary.
+ *
+ * Beams of one prompt share its blocks and part ways copy on write ("PagedAttention:
+ * The vLLM Paper", "Implementation Essentials", prefix sharing); the pages leave
+ * the selection to the sampler. For sequence b with num_beams running beams,
+ *   score[k][v] = beam_scores[b][k] + x[k][v] - log sum_u exp(x[k][u]),
+ * x the logits of row b * num_beams + k, the num_select largest scores of all
+ * (k, v), best first, ties to the smaller k * vocab + v: their scores, beams and
+ * tokens. Scores are ranked in double precision and rounded to float. A score
+ * of -inf is no candidate: a beam score of -inf (an ended beam, or all but one
+ * before the first step) or a logit of -inf (a masked token) takes it out. A beam
+ * with a NaN or +inf among its logits, or as its score, gives no candidates
+ * (PA_DEVERR_LOGITS). Places left over get score -inf, parent -1, token -1.
+ *
+ *   scores, parents, tokens   device, float / int32 / int32 [num_seqs][num_select]
+ *   logits        device, [num_seqs * num_beams][vocab] of type dtype (PA_F16,
+ *                 PA_BF16 or PA_F32), rows row_stride elements apart (>= vocab and
+ *                 rows of a multiple of 16 bytes); 16-byte aligned
+ *   beam_scores   device, float [num_seqs][num_beams]
+ *   num_beams     1 .. PA_BEAM_MAX
+ *   num_select    1 .. PA_BEAM_MAX (2 * beams leave as many after ended ones)
+ *   vocab         1 .. 2^24
+ *   workspace     device scratch of pa_beam_select_workspace_size() bytes, 256-byte
+ *                 aligned; needs no initial value. Calls that run concurrently
+ *                 need separate workspaces
+ *   dev_error     device int or NULL
+ * The outputs must not overlap the inputs. num_seqs == 0 is a no-op. After it,
+ * pa_bm_reorder makes the sequences continue their parents.
+ * ------------------------------------------------------------------------- */
+#define PA_BEAM_MAX 64
+int pa_beam_select_workspace_size(int num_seqs, int num_beams, int vocab, int num_select, int dtype,
+                                  size_t* bytes);
+
+int pa_beam_select(float* scores, int32_t* parents, int32_t* tokens, const void* logits,
+                   int64_t row_stride, const float* beam_scores, int num_seqs, int num_beams,
+                   int vocab, int num_select, void* workspace, size_t workspace_bytes,
+                   int* dev_error, int dtype, void* stream);
 
 /* ---------------------------------------------------------------------------
  * pa_paged_decode — decode-step attention through the block tables.
@@ -613,6 +660,16 @@ int pa_bm_add_seq(pa_bm* bm, int64_t seq_id, int num_tokens, int64_t* slots_out)
 
 /* child shares every block of parent (refcounts + 1). */
 int pa_bm_fork(pa_bm* bm, int64_t parent, int64_t child);
+
+/* The reordering after a beam-search step: sequence seq_ids[i] becomes a copy of
+ * what sequence seq_ids[parents[i]] was before the call (its length and, sharing
+ * every block, its table), for all i at once; parents[i] == i or -1 keeps
+ * sequence i. Only host state changes: keys and values stay where they are, and
+ * later appends copy shared partly filled blocks on write. Blocks left without
+ * a holder are released in the order of i, each sequence's from its last logical
+ * block to its first. seq_ids are registered, distinct and not swapped out;
+ * parents in [-1, n). Takes no blocks, so it cannot run out of them. */
+int pa_bm_reorder(pa_bm* bm, const int64_t* seq_ids, const int32_t* parents, int n);
 
 /* Append n tokens to seq_id: slots_out[n]; cow_pairs_out[2] receives at most one
  * (src, dst) pair and *n_cow its count (0 or 1). */

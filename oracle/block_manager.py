@@ -321,6 +321,30 @@ class BlockManager:
         self._tables[child] = table
         self._lens[child] = self._lens[parent]
 
+    def reorder(self, seq_ids, parents) -> None:
+        """Sequence ``seq_ids[i]`` becomes a copy of what ``seq_ids[parents[i]]`` was, for all
+        ``i`` at once (a parent of ``i`` itself or -1 changes nothing): the step of a beam
+        search after its selection. The pages name beams only as sharers of a prompt's blocks
+        ("PagedAttention: The vLLM Paper", "Implementation Essentials"); the order in which
+        blocks without a holder are released is this reading's: by ``i``, last block first."""
+        seq_ids, parents = list(seq_ids), list(parents)
+        for s in seq_ids:
+            self._need(s)
+            self._resident(s)
+        if len(set(seq_ids)) != len(seq_ids) or any(not -1 <= p < len(seq_ids) for p in parents):
+            raise BlockManagerError(ERR_INVALID_ARG, "duplicate sequence or bad parent")
+        was = [(list(self._tables[s]), self._lens[s]) for s in seq_ids]
+        moves = [i for i, p in enumerate(parents) if p not in (-1, i)]
+        for i in moves:
+            for b in was[parents[i]][0]:
+                self._ref[b] += 1
+        for i in moves:
+            self._tables[seq_ids[i]] = list(was[parents[i]][0])
+            self._lens[seq_ids[i]] = was[parents[i]][1]
+        for i in moves:
+            for b in reversed(was[i][0]):
+                self._release(b)
+
     def append_slots(self, seq_id: int, n: int):
         """Append ``n`` tokens; return ``(slots, cow_pairs)``."""
         self._need(seq_id)

@@ -30,6 +30,7 @@ PA_F16 = 0
 PA_BF16 = 1
 PA_FP8_E4M3 = 2
 PA_INT4 = 3
+PA_F32 = 4
 
 PA_DEVERR_SLOT_RANGE = 1
 PA_DEVERR_BLOCK_RANGE = 2
@@ -37,6 +38,7 @@ PA_DEVERR_CONTEXT_RANGE = 4
 PA_DEVERR_WAIT_TIMEOUT = 8
 PA_DEVERR_GROUP = 16
 PA_DEVERR_POSITION = 32
+PA_DEVERR_LOGITS = 64
 
 BLOCK_SIZE = 16
 
@@ -90,6 +92,10 @@ _SIGS = {
     "pa_rope_and_cache_fp8": (_c_int, _ROPE_ARGS + [ctypes.c_float, ctypes.c_float, _vp, _vp]),
     "pa_rope_and_cache_int4": (_c_int, _ROPE_ARGS + [_vp, _vp]),
     "pa_rope_table": (_c_int, [_vp, _c_int, _c_int, ctypes.c_double]),
+    "pa_beam_select_workspace_size": (_c_int, [_c_int] * 5 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "pa_beam_select": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _vp, _c_int, _c_int, _c_int, _c_int,
+                                _vp, ctypes.c_size_t, _vp, _c_int, _vp]),
+    "pa_bm_reorder": (_c_int, [_vp, _vp, _vp, _c_int]),
     "pa_paged_decode_cascade_workspace_size": (_c_int, [_c_int] * 10 +
                                                 [ctypes.POINTER(ctypes.c_size_t)]),
     "pa_paged_decode_cascade": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int,
@@ -629,6 +635,65 @@ def pa_rope_and_cache_int4(q_out, q, key, value, positions, cos_sin, k_cache, v_
           positions, cos_sin, k_cache, v_cache, slot_mapping, interleaved, (), dev_error, stream)
 
 
+def _logits_code(dtype) -> int:
+    torch = _torch()
+    code = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}.get(dtype)
+    if code is None:
+        raise PAError(PA_ERR_UNSUPPORTED, f"logits of type {dtype}: expected float16, bfloat16 or "
+                                          "float32")
+    return code
+
+
+def pa_beam_select_workspace_size(num_seqs, num_beams, vocab, num_select, dtype=PA_F32) -> int:
+    """Workspace bytes of ``pa_beam_select`` over logits of type ``dtype`` (a code)."""
+    n = ctypes.c_size_t(0)
+    _check(lib().pa_beam_select_workspace_size(int(num_seqs), int(num_beams), int(vocab),
+                                               int(num_select), int(dtype), ctypes.byref(n)))
+    return n.value
+
+
+def beam_workspace(num_seqs, num_beams, vocab, num_select, device=None):
+    """A workspace tensor large enough for ``pa_beam_select`` over logits of any type."""
+    torch = _torch()
+    n = max(pa_beam_select_workspace_size(num_seqs, num_beams, vocab, num_select, code)
+            for code in (PA_F16, PA_F32))
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_beam_select(scores, parents, tokens, logits, beam_scores, workspace, dev_error=None,
+                   stream=None):
+    """The best continuations of every sequence's beams: ``logits`` ``[B * K, V]``
+    (float16, bfloat16 or float32; rows may be padded), ``beam_scores`` float32
+    ``[B, K]``; writes ``scores`` float32, ``parents`` and ``tokens`` int32, all
+    ``[B, num_select]``, best first (-inf, -1, -1 where candidates run out)."""
+    torch = _torch()
+    if beam_scores.dim() != 2 or logits.dim() != 2 or scores.dim() != 2:
+        raise PAError(PA_ERR_INVALID_ARG, "beam_scores must be [B, K], logits [B * K, V], scores "
+                                          "[B, num_select]")
+    B, K = beam_scores.shape
+    rows, V = logits.shape
+    n = scores.shape[1]
+    if (rows != B * K or scores.shape[0] != B or parents.shape != scores.shape or
+            tokens.shape != scores.shape):
+        raise PAError(PA_ERR_INVALID_ARG, "logits must be [B * K, V]; scores, parents and tokens "
+                                          "[B, num_select]")
+    if rows and V > 1 and logits.stride(1) != 1:
+        raise PAError(PA_ERR_INVALID_ARG, "logits rows must be dense")
+    per16 = 4 if logits.dtype == torch.float32 else 8
+    # one row's stride is not used: any that holds it will do
+    stride = logits.stride(0) if rows > 1 else -(-V // per16) * per16
+    _same_device(scores, parents, tokens, logits, beam_scores, workspace, dev_error)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _device(logits):
+        _check(lib().pa_beam_select(
+            _dev_ptr(scores, "scores", torch.float32), _dev_ptr(parents, "parents", torch.int32),
+            _dev_ptr(tokens, "tokens", torch.int32), _dev_ptr(logits, "logits", contiguous=False),
+            stride, _dev_ptr(beam_scores, "beam_scores", torch.float32), B, K, V, n,
+            _dev_ptr(workspace, "workspace"), ws_bytes,
+            _dev_ptr(dev_error, "dev_error", torch.int32), _logits_code(logits.dtype),
+            _stream(stream)))
+
+
 def pa_paged_decode_cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                            max_context_len, max_blocks_per_seq, num_groups,
                                            group_size, max_prefix_blocks) -> int:
@@ -820,6 +885,16 @@ class BlockManager:
 
     def fork(self, parent: int, child: int) -> None:
         _check(self._lib.pa_bm_fork(self._h, parent, child))
+
+    def reorder(self, seq_ids, parents) -> None:
+        """After a beam-search step: sequence ``seq_ids[i]`` becomes a copy of what sequence
+        ``seq_ids[parents[i]]`` was (-1 or ``i``: stays), sharing its blocks."""
+        ids = np.ascontiguousarray(np.asarray(seq_ids, np.int64))
+        par = np.ascontiguousarray(np.asarray(parents, np.int32))
+        if ids.ndim != 1 or par.shape != ids.shape:
+            raise PAError(PA_ERR_INVALID_ARG, "seq_ids and parents must be lists of one length")
+        _check(self._lib.pa_bm_reorder(self._h, ids.ctypes.data if len(ids) else None,
+                                       par.ctypes.data if len(ids) else None, len(ids)))
 
     def append_slots(self, seq_id: int, n: int):
         slots = np.empty(max(n, 0), np.int64)

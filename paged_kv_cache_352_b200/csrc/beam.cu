@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kBeamThreads = 256;
 constexpr int kGroups = 64;       // groups of a tile whose maxima bound the N-th largest
-constexpr int kTileCap = 1024;    // candidates a tile ranks at once
+constexpr int kTileCap = 2048;    // candidates a tile ranks at once
 constexpr int kMergeThreads = 512;
 constexpr int kMergeCap = 2048;   // candidates a sequence ranks at once
 
@@ -45,9 +45,9 @@ __device__ __forceinline__ float from_orderable(uint32_t k) {
 }
 
 // (value, index) as one key: larger is better, ties to the smaller index. 0 is
-// below every candidate.
+// below every candidate. -0 counts as 0.
 __device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
-  return ((uint64_t)orderable(x) << 32) | (uint32_t)~index;
+  return ((uint64_t)orderable(__fadd_rn(x, 0.f)) << 32) | (uint32_t)~index;
 }
 
 // EPL elements of the logits type per 16-byte load, widened
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kBeamThreads)
   __shared__ uint64_t cand[kTileCap];
   __shared__ uint32_t threshold;
   __shared__ int count;
-  const int tile = blockIdx.x, row = blockIdx.y;
+  const int row = blockIdx.x / tiles, tile = blockIdx.x - row * tiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const T* x = logits + (int64_t)row * row_stride;
   const int base = tile * kBeamThreads * kPer;
@@ -210,11 +210,7 @@ __global__ void __launch_bounds__(kBeamThreads)
   }
 }
 
-// Larger is better, ties to the smaller flat index.
-struct Cand {
-  double score;
-  int64_t flat;
-};
+// Candidates are ordered by score, ties to the smaller flat index.
 __device__ __forceinline__ bool before(double s, int64_t f, double t, int64_t g) {
   return s > t || (s == t && f < g);
 }
@@ -232,7 +228,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   __shared__ double offset[PA_BEAM_MAX];  // beam score less logsumexp, -inf for a dead beam
   __shared__ double cs[kMergeCap];
   __shared__ int64_t cf[kMergeCap];
-  __shared__ double maxima[kMergeThreads];
+  __shared__ double group_max[kGroups];
   __shared__ double threshold;
   __shared__ int count;
   const int b = blockIdx.x;
@@ -275,28 +271,36 @@ __global__ void __launch_bounds__(kMergeThreads)
       f = (int64_t)k * vocab + (uint32_t)~(uint32_t)key;
     }
   };
-  double lowest = -INFINITY;
-  if (total > kMergeCap) {
-    // the select-th largest of the threads' maxima bounds the result from below
-    double m = -INFINITY;
-    for (int i = threadIdx.x; i < total; i += kMergeThreads) {
-      double s;
-      int64_t f;
-      score_of(i, s, f);
-      m = fmax(m, s);
-    }
-    maxima[threadIdx.x] = m;
-    if (threadIdx.x == 0) threshold = -INFINITY;
-    __syncthreads();
-    int at_least = 0, above = 0;
-    for (int j = 0; j < kMergeThreads; ++j) {
-      at_least += maxima[j] >= m;
-      above += maxima[j] > m;
-    }
-    if (at_least >= select && above < select) threshold = m;  // one value
-    __syncthreads();
-    lowest = threshold;
+  // as in a tile: the select-th largest of 64 groups' maxima bounds the result from below
+  double top = -INFINITY;
+  for (int i = threadIdx.x; i < total; i += kMergeThreads) {
+    double s;
+    int64_t f;
+    score_of(i, s, f);
+    top = fmax(top, s);
   }
+  constexpr int kGroupLanes = kMergeThreads / kGroups;
+#pragma unroll
+  for (int mask = 1; mask < kGroupLanes; mask <<= 1)
+    top = fmax(top, __shfl_xor_sync(0xffffffffu, top, mask));
+  if (threadIdx.x % kGroupLanes == 0) group_max[threadIdx.x / kGroupLanes] = top;
+  __syncthreads();
+  if (warp == 0) {
+    const double p = group_max[lane], q = group_max[lane + 32];
+    int rp = 0, rq = 0;
+#pragma unroll 8
+    for (int i = 0; i < kGroups; ++i) {
+      rp += group_max[i] >= p;
+      rq += group_max[i] >= q;
+    }
+    double best = fmax(rp >= select ? p : -INFINITY, rq >= select ? q : -INFINITY);
+#pragma unroll
+    for (int mask = 16; mask > 0; mask >>= 1)
+      best = fmax(best, __shfl_xor_sync(0xffffffffu, best, mask));
+    if (lane == 0) threshold = best;
+  }
+  __syncthreads();
+  const double lowest = threshold;
   for (int i = threadIdx.x; i < total; i += kMergeThreads) {
     double s;
     int64_t f;
@@ -408,7 +412,9 @@ cudaError_t launch_beam_select(const BeamArgs& a, int dtype, cudaStream_t stream
   float* tm = reinterpret_cast<float*>(ws + lay.max_off);
   float* ts = reinterpret_cast<float*>(ws + lay.sum_off);
   uint64_t* tk = reinterpret_cast<uint64_t*>(ws + lay.key_off);
-  const dim3 grid(lay.tiles, a.num_seqs * a.num_beams);
+  const int64_t ctas = (int64_t)lay.tiles * a.num_seqs * a.num_beams;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)ctas);
   auto go = [&](auto kern, auto* x) {
     return launch_dependent(kern, grid, dim3(kBeamThreads), 0, stream, x, a.row_stride, a.vocab,
                             a.select, lay.tiles, tm, ts, tk);

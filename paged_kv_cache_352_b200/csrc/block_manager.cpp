@@ -133,6 +133,47 @@ int pa_bm_fork(pa_bm* bm, int64_t parent, int64_t child) {
   return PA_OK;
 }
 
+int pa_bm_reorder(pa_bm* bm, const int64_t* seq_ids, const int32_t* parents, int n) {
+  pa::clear_error();
+  if (!bm) return fail(PA_ERR_INVALID_ARG, "null manager");
+  if (n < 0) return fail(PA_ERR_INVALID_ARG, "n must be >= 0");
+  if (n == 0) return PA_OK;
+  if (!seq_ids || !parents) return fail(PA_ERR_INVALID_ARG, "null pointer argument");
+  std::vector<pa_bm::Seq*> seqs;
+  std::vector<pa_bm::Seq> next;  // what the sequences become; then what they were
+  try {
+    seqs.resize(n);
+    next.resize(n);
+    std::set<int64_t> ids;
+    for (int i = 0; i < n; ++i) {
+      auto it = bm->seqs.find(seq_ids[i]);
+      if (it == bm->seqs.end())
+        return fail(PA_ERR_UNKNOWN_SEQ, "unknown sequence %lld", (long long)seq_ids[i]);
+      if (it->second.swapped) return swapped_error(seq_ids[i]);
+      if (!ids.insert(seq_ids[i]).second)
+        return fail(PA_ERR_INVALID_ARG, "sequence %lld appears twice", (long long)seq_ids[i]);
+      if (parents[i] < -1 || parents[i] >= n)
+        return fail(PA_ERR_INVALID_ARG, "parents[%d] = %d: expected -1 .. %d", i, parents[i],
+                    n - 1);
+      seqs[i] = &it->second;
+    }
+    for (int i = 0; i < n; ++i)
+      if (parents[i] >= 0 && parents[i] != i) next[i] = *seqs[parents[i]];
+  } catch (const std::bad_alloc&) {
+    return fail(PA_ERR_INVALID_ARG, "out of host memory");
+  }
+  auto moves = [&](int i) { return parents[i] >= 0 && parents[i] != i; };
+  for (int i = 0; i < n; ++i)  // hold the new blocks before any old one is let go
+    if (moves(i))
+      for (int32_t b : next[i].table) ++bm->ref[b];
+  for (int i = 0; i < n; ++i)
+    if (moves(i)) std::swap(*seqs[i], next[i]);
+  for (int i = 0; i < n; ++i)
+    if (moves(i))
+      for (auto b = next[i].table.rbegin(); b != next[i].table.rend(); ++b) bm->release(*b);
+  return PA_OK;
+}
+
 int pa_bm_append_slots(pa_bm* bm, int64_t seq_id, int n, int64_t* slots_out,
                        int64_t* cow_pairs_out, int* n_cow) {
   pa::clear_error();

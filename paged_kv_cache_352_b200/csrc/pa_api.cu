@@ -1130,4 +1130,72 @@ int pa_rope_and_cache_int4(void* q_out, const void* q, const void* key, const vo
 
 #undef PA_ROPE_ARGS
 
+// The checks pa_beam_select shares with its workspace size.
+static int check_beam_sizes(int num_seqs, int num_beams, int vocab, int num_select, int dtype) {
+  if (dtype != PA_F16 && dtype != PA_BF16 && dtype != PA_F32)
+    return fail(PA_ERR_UNSUPPORTED, "dtype %d: expected PA_F16, PA_BF16 or PA_F32", dtype);
+  if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs must be >= 0");
+  if (num_beams < 1 || num_beams > PA_BEAM_MAX || num_select < 1 || num_select > PA_BEAM_MAX)
+    return fail(PA_ERR_UNSUPPORTED, "num_beams %d, num_select %d: expected 1 .. %d", num_beams,
+                num_select, PA_BEAM_MAX);
+  if (vocab < 1 || vocab > (1 << 24))
+    return fail(PA_ERR_UNSUPPORTED, "vocab %d: expected 1 .. 2^24", vocab);
+  BeamLayout lay;
+  beam_layout(num_seqs, num_beams, vocab, num_select, dtype, &lay);
+  if ((long long)num_seqs * num_beams * lay.tiles > 0x7fffffffLL)
+    return fail(PA_ERR_UNSUPPORTED, "num_seqs x num_beams x vocab exceeds the grid limit");
+  return PA_OK;
+}
+
+int pa_beam_select_workspace_size(int num_seqs, int num_beams, int vocab, int num_select, int dtype,
+                                  size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(PA_ERR_INVALID_ARG, "bytes must not be NULL");
+  if (int st = check_beam_sizes(num_seqs, num_beams, vocab, num_select, dtype)) return st;
+  BeamLayout lay;
+  beam_layout(num_seqs, num_beams, vocab, num_select, dtype, &lay);
+  *bytes = lay.bytes;
+  return PA_OK;
+}
+
+int pa_beam_select(float* scores, int32_t* parents, int32_t* tokens, const void* logits,
+                   int64_t row_stride, const float* beam_scores, int num_seqs, int num_beams,
+                   int vocab, int num_select, void* workspace, size_t workspace_bytes,
+                   int* dev_error, int dtype, void* stream) {
+  const NvtxRange nvtx_range("pa_beam_select");
+  clear_error();
+  if (int st = check_beam_sizes(num_seqs, num_beams, vocab, num_select, dtype)) return st;
+  if (num_seqs == 0) return PA_OK;
+  if (!scores || !parents || !tokens || !logits || !beam_scores)
+    return fail(PA_ERR_INVALID_ARG, "null pointer argument");
+  const int per16 = dtype == PA_F32 ? 4 : 8;
+  if (row_stride < vocab || row_stride % per16)
+    return fail(PA_ERR_INVALID_ARG,
+                "row_stride %lld must be >= vocab (%d) and a multiple of %d elements (16 bytes)",
+                (long long)row_stride, vocab, per16);
+  if (!aligned16(logits)) return fail(PA_ERR_INVALID_ARG, "logits must be 16-byte aligned");
+  BeamLayout lay;
+  beam_layout(num_seqs, num_beams, vocab, num_select, dtype, &lay);
+  if (!workspace || workspace_bytes < lay.bytes)
+    return fail(PA_ERR_INVALID_ARG, "workspace of %zu bytes needed, %zu given", lay.bytes,
+                workspace ? workspace_bytes : (size_t)0);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(PA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  BeamArgs a;
+  a.scores = scores;
+  a.parents = parents;
+  a.tokens = tokens;
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.beam_scores = beam_scores;
+  a.num_seqs = num_seqs;
+  a.num_beams = num_beams;
+  a.vocab = vocab;
+  a.select = num_select;
+  a.workspace = workspace;
+  a.dev_error = dev_error;
+  return cuda_status(launch_beam_select(a, dtype, static_cast<cudaStream_t>(stream)),
+                     "beam_select launch");
+}
+
 }  // extern "C"

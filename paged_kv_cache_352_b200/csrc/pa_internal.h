@@ -184,6 +184,27 @@ cudaError_t launch_read_slots_int4(void* key, void* value, int64_t key_stride,
                                    int head_dim, int num_blocks, int dtype, int* dev_error,
                                    cudaStream_t stream);
 
+// Beam selection: arguments as pa_beam_select takes them.
+struct BeamArgs {
+  float* scores;
+  int32_t* parents;
+  int32_t* tokens;
+  const void* logits;
+  int64_t row_stride;
+  const float* beam_scores;
+  int num_seqs, num_beams, vocab, select;
+  void* workspace;
+  int* dev_error;
+};
+// Workspace: per (row, tile) a maximum, a sum of exponentials and `select` keys.
+struct BeamLayout {
+  bool large;  // tile size
+  int tiles;   // tiles per row
+  size_t max_off, sum_off, key_off, bytes;
+};
+void beam_layout(int num_seqs, int num_beams, int vocab, int select, int dtype, BeamLayout* lay);
+cudaError_t launch_beam_select(const BeamArgs& a, int dtype, cudaStream_t stream);
+
 // Cascade decode of sequences that share leading blocks: the prefix states of
 // every group come from one decode over the shared blocks (the members' query
 // heads stacked as one KV head's group), the rest of each sequence from its own
