@@ -189,9 +189,15 @@ def _check(status: int):
 # tensor marshalling
 # --------------------------------------------------------------------------
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def dtype_code(t) -> int:
@@ -265,28 +271,56 @@ def _int4_dims(k_cache, v_cache):
     return nb, hkv, bs, d
 
 
+class _On:
+    """The device of a call's tensors: ``ptr`` gives a tensor's address after checking that it
+    lies there, and ``call`` runs a library call with that device current, on the given
+    stream or the device's current one."""
+
+    def __init__(self, t):
+        self.dev = t.device
+        if self.dev.type != "cuda":
+            raise PAError(PA_ERR_INVALID_ARG, f"tensors must be on a CUDA device, got {self.dev}")
+
+    def ptr(self, t, name, dtype=None, contiguous=True):
+        if t is None:
+            return None
+        if t.device != self.dev:
+            raise PAError(PA_ERR_INVALID_ARG, f"{name} is on {t.device}, expected {self.dev}")
+        if dtype is not None and t.dtype is not dtype:
+            raise PAError(PA_ERR_INVALID_ARG, f"{name} must be {dtype}, got {t.dtype}")
+        if contiguous and not t.is_contiguous():
+            raise PAError(PA_ERR_INVALID_ARG, f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def rows(self, t, name, heads, d, dtype=None):
+        """Address and token stride of a [T, heads, d] tensor whose rows are dense per token (the
+        stride of a dense one when T is 1, where a tensor's own may be anything)."""
+        T = t.shape[0]
+        stride = t.stride()
+        if T and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
+            raise PAError(PA_ERR_INVALID_ARG, f"{name} rows must be dense per token")
+        return self.ptr(t, name, dtype, False), (stride[0] if T > 1 else heads * d)
+
+    def call(self, fn, *args, stream=None):
+        torch = _torch()
+        idx = self.dev.index
+        if torch.cuda.current_device() == idx:
+            return _check(fn(*args, _raw_stream(stream, idx)))
+        with torch.cuda.device(idx):
+            return _check(fn(*args, _raw_stream(stream, idx)))
+
+
+def _raw_stream(stream, index):
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _check_rows(key, value, hkv, d):
     T = key.shape[0]
-    if key.shape[1:] != (hkv, d) or value.shape[1:] != (hkv, d) or value.shape[0] != T:
+    if key.shape[1:] != (hkv, d) or value.shape != key.shape:
         raise PAError(PA_ERR_INVALID_ARG, "key/value must be [T, num_kv_heads, head_dim]")
-    for x in (key, value):
-        if T and (x.stride(2) != 1 or (hkv > 1 and x.stride(1) != d)):
-            raise PAError(PA_ERR_INVALID_ARG, "key/value rows must be dense per token")
-    if value.dtype != key.dtype:
-        raise PAError(PA_ERR_INVALID_ARG, "value must be of key's dtype")
     return T
-
-
-def _token_stride(x):
-    """Token stride of a [T, H, d] tensor: that of a dense one when T is 1, where a tensor's own
-    may be anything."""
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
-
-
-def _same_device(*tensors):
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) > 1:
-        raise PAError(PA_ERR_INVALID_ARG, f"tensors on different devices: {sorted(map(str, devs))}")
 
 
 # --------------------------------------------------------------------------
@@ -502,43 +536,35 @@ def pa_paged_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, ma
             _stream(stream)))
 
 
-def pa_reshape_and_cache_int4(key, value, k_cache, v_cache, slot_mapping, dev_error=None,
-                              stream=None):
-    """Quantize ``key``/``value`` ``[T, num_kv_heads, head_dim]`` (float16/bfloat16)
-    into the 4-bit caches (uint8 ``[num_blocks, num_kv_heads, 16, head_dim/2 + 4]``)
-    at ``slot_mapping`` (int64 [T])."""
+def _int4_rows(fn, key, value, k_cache, v_cache, slot_mapping, dev_error, stream):
     torch = _torch()
     nb, hkv, bs, d = _int4_dims(k_cache, v_cache)
     T = _check_rows(key, value, hkv, d)
     if slot_mapping.shape != (T,):
         raise PAError(PA_ERR_INVALID_ARG, "slot_mapping must be [T]")
-    _same_device(key, value, k_cache, v_cache, slot_mapping, dev_error)
-    with _device(k_cache):
-        _check(lib().pa_reshape_and_cache_int4(
-            _dev_ptr(key, "key", contiguous=False), _dev_ptr(value, "value", contiguous=False),
-            _token_stride(key), _token_stride(value), _dev_ptr(k_cache, "k_cache"),
-            _dev_ptr(v_cache, "v_cache"), _dev_ptr(slot_mapping, "slot_mapping", torch.int64), T,
-            hkv, d, bs, nb, dtype_code(key), _dev_ptr(dev_error, "dev_error", torch.int32),
-            _stream(stream)))
+    on = _On(k_cache)
+    kp, ks = on.rows(key, "key", hkv, d)
+    vp, vs = on.rows(value, "value", hkv, d, key.dtype)
+    on.call(fn, kp, vp, ks, vs, on.ptr(k_cache, "k_cache"), on.ptr(v_cache, "v_cache"),
+            on.ptr(slot_mapping, "slot_mapping", torch.int64), T, hkv, d, bs, nb, dtype_code(key),
+            on.ptr(dev_error, "dev_error", torch.int32), stream=stream)
+
+
+def pa_reshape_and_cache_int4(key, value, k_cache, v_cache, slot_mapping, dev_error=None,
+                              stream=None):
+    """Quantize ``key``/``value`` ``[T, num_kv_heads, head_dim]`` (float16/bfloat16)
+    into the 4-bit caches (uint8 ``[num_blocks, num_kv_heads, 16, head_dim/2 + 4]``)
+    at ``slot_mapping`` (int64 [T])."""
+    _int4_rows(lib().pa_reshape_and_cache_int4, key, value, k_cache, v_cache, slot_mapping,
+               dev_error, stream)
 
 
 def pa_read_slots_int4(key, value, k_cache, v_cache, slot_mapping, dev_error=None, stream=None):
     """Write the values held at ``slot_mapping`` (int64 [T]) of 4-bit caches into
     ``key``/``value`` ``[T, num_kv_heads, head_dim]`` (float16/bfloat16); rows with a
     negative slot stay as they were."""
-    torch = _torch()
-    nb, hkv, bs, d = _int4_dims(k_cache, v_cache)
-    T = _check_rows(key, value, hkv, d)
-    if slot_mapping.shape != (T,):
-        raise PAError(PA_ERR_INVALID_ARG, "slot_mapping must be [T]")
-    _same_device(key, value, k_cache, v_cache, slot_mapping, dev_error)
-    with _device(k_cache):
-        _check(lib().pa_read_slots_int4(
-            _dev_ptr(key, "key", contiguous=False), _dev_ptr(value, "value", contiguous=False),
-            _token_stride(key), _token_stride(value), _dev_ptr(k_cache, "k_cache"),
-            _dev_ptr(v_cache, "v_cache"), _dev_ptr(slot_mapping, "slot_mapping", torch.int64), T,
-            hkv, d, bs, nb, dtype_code(key), _dev_ptr(dev_error, "dev_error", torch.int32),
-            _stream(stream)))
+    _int4_rows(lib().pa_read_slots_int4, key, value, k_cache, v_cache, slot_mapping, dev_error,
+               stream)
 
 
 def pa_paged_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, max_context_len,
@@ -548,22 +574,22 @@ def pa_paged_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, m
     head_dim/2 + 4]``); ``q``/``out`` are float16 or bfloat16."""
     torch = _torch()
     nb, hkv, bs, d = _int4_dims(k_cache, v_cache)
-    if q.dim() != 3 or q.shape[2] != d or out.shape != q.shape or out.dtype != q.dtype:
+    if q.dim() != 3 or q.shape[2] != d or out.shape != q.shape:
         raise PAError(PA_ERR_INVALID_ARG, "q/out must be [B, num_q_heads, head_dim], one dtype")
     B, hq, _ = q.shape
     if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
         raise PAError(PA_ERR_INVALID_ARG, "block_tables must be [B, max_blocks], context_lens [B]")
-    _same_device(out, q, k_cache, v_cache, block_tables, context_lens, workspace, dev_error,
-                 seq_order)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _device(q):
-        _check(lib().pa_paged_decode_int4(
-            _dev_ptr(out, "out"), _dev_ptr(q, "q"), _dev_ptr(k_cache, "k_cache"),
-            _dev_ptr(v_cache, "v_cache"), _dev_ptr(block_tables, "block_tables", torch.int32),
-            block_tables.shape[1], _dev_ptr(context_lens, "context_lens", torch.int32),
-            _order_ptr(seq_order, B), B, int(max_context_len), hq, hkv, d, bs, nb, float(scale),
-            int(partition_tokens), _dev_ptr(workspace, "workspace"), ws_bytes,
-            _dev_ptr(dev_error, "dev_error", torch.int32), dtype_code(q), _stream(stream)))
+    if seq_order is not None and seq_order.shape != (B,):
+        raise PAError(PA_ERR_INVALID_ARG, "seq_order must be [num_seqs]")
+    on = _On(q)
+    i32 = torch.int32
+    on.call(lib().pa_paged_decode_int4, on.ptr(out, "out", q.dtype), on.ptr(q, "q"),
+            on.ptr(k_cache, "k_cache"), on.ptr(v_cache, "v_cache"),
+            on.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
+            on.ptr(context_lens, "context_lens", i32), on.ptr(seq_order, "seq_order", i32), B,
+            int(max_context_len), hq, hkv, d, bs, nb, scale, int(partition_tokens),
+            on.ptr(workspace, "workspace"), 0 if workspace is None else workspace.nbytes,
+            on.ptr(dev_error, "dev_error", i32), dtype_code(q), stream=stream)
 
 
 def pa_rope_table(num_positions, rotary_dim, theta=10000.0) -> np.ndarray:
@@ -575,37 +601,31 @@ def pa_rope_table(num_positions, rotary_dim, theta=10000.0) -> np.ndarray:
     return table
 
 
-def _rope(call, dims, cache_ok, q_out, q, key, value, positions, cos_sin, k_cache, v_cache,
+def _rope(fn, dims, cache_ok, q_out, q, key, value, positions, cos_sin, k_cache, v_cache,
           slot_mapping, interleaved, scales, dev_error, stream):
     torch = _torch()
     nb, hkv, bs, d = dims
     T = _check_rows(key, value, hkv, d)
     if not cache_ok:
         raise PAError(PA_ERR_INVALID_ARG, "k_cache/v_cache are not of the call's element type")
-    if (q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or q_out.shape != q.shape or
-            q.dtype != key.dtype or q_out.dtype != key.dtype):
+    if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or q_out.shape != q.shape:
         raise PAError(PA_ERR_INVALID_ARG, "q/q_out must be [T, num_q_heads, head_dim] in key's "
                                           "dtype")
-    hq = q.shape[1]
-    for x in (q, q_out):
-        if T and (x.stride(2) != 1 or (hq > 1 and x.stride(1) != d)):
-            raise PAError(PA_ERR_INVALID_ARG, "q/q_out rows must be dense per token")
     if positions.shape != (T,) or slot_mapping.shape != (T,) or cos_sin.dim() != 2:
         raise PAError(PA_ERR_INVALID_ARG, "positions and slot_mapping must be [T], cos_sin "
                                           "[num_positions, rotary_dim]")
-    _same_device(q_out, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping,
-                 dev_error)
-    with _device(k_cache):
-        _check(call(
-            _dev_ptr(q_out, "q_out", contiguous=False), _dev_ptr(q, "q", contiguous=False),
-            _dev_ptr(key, "key", contiguous=False), _dev_ptr(value, "value", contiguous=False),
-            _token_stride(q_out), _token_stride(q), _token_stride(key), _token_stride(value),
-            _dev_ptr(positions, "positions", torch.int64),
-            _dev_ptr(cos_sin, "cos_sin", torch.float32), cos_sin.shape[0], cos_sin.shape[1],
-            int(bool(interleaved)), _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), T, hq, hkv, d, bs, nb,
-            dtype_code(key), *scales, _dev_ptr(dev_error, "dev_error", torch.int32),
-            _stream(stream)))
+    on = _On(k_cache)
+    hq, dt = q.shape[1], key.dtype
+    qop, qos = on.rows(q_out, "q_out", hq, d, dt)
+    qp, qs = on.rows(q, "q", hq, d, dt)
+    kp, ks = on.rows(key, "key", hkv, d)
+    vp, vs = on.rows(value, "value", hkv, d, dt)
+    P, R = cos_sin.shape
+    on.call(fn, qop, qp, kp, vp, qos, qs, ks, vs, on.ptr(positions, "positions", torch.int64),
+            on.ptr(cos_sin, "cos_sin", torch.float32), P, R, int(bool(interleaved)),
+            on.ptr(k_cache, "k_cache"), on.ptr(v_cache, "v_cache"),
+            on.ptr(slot_mapping, "slot_mapping", torch.int64), T, hq, hkv, d, bs, nb,
+            dtype_code(key), *scales, on.ptr(dev_error, "dev_error", torch.int32), stream=stream)
 
 
 def pa_rope_and_cache(q_out, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping,
@@ -682,16 +702,13 @@ def pa_beam_select(scores, parents, tokens, logits, beam_scores, workspace, dev_
     per16 = 4 if logits.dtype == torch.float32 else 8
     # one row's stride is not used: any that holds it will do
     stride = logits.stride(0) if rows > 1 else -(-V // per16) * per16
-    _same_device(scores, parents, tokens, logits, beam_scores, workspace, dev_error)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _device(logits):
-        _check(lib().pa_beam_select(
-            _dev_ptr(scores, "scores", torch.float32), _dev_ptr(parents, "parents", torch.int32),
-            _dev_ptr(tokens, "tokens", torch.int32), _dev_ptr(logits, "logits", contiguous=False),
-            stride, _dev_ptr(beam_scores, "beam_scores", torch.float32), B, K, V, n,
-            _dev_ptr(workspace, "workspace"), ws_bytes,
-            _dev_ptr(dev_error, "dev_error", torch.int32), _logits_code(logits.dtype),
-            _stream(stream)))
+    on = _On(logits)
+    f32, i32 = torch.float32, torch.int32
+    on.call(lib().pa_beam_select, on.ptr(scores, "scores", f32), on.ptr(parents, "parents", i32),
+            on.ptr(tokens, "tokens", i32), on.ptr(logits, "logits", None, False), stride,
+            on.ptr(beam_scores, "beam_scores", f32), B, K, V, n, on.ptr(workspace, "workspace"),
+            0 if workspace is None else workspace.nbytes, on.ptr(dev_error, "dev_error", i32),
+            _logits_code(logits.dtype), stream=stream)
 
 
 def pa_paged_decode_cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,

@@ -22,6 +22,9 @@
 // sums are fp32 per thread (at most kPer terms), double from there on.
 #include <cuda_runtime.h>
 #include <math.h>
+#include <string.h>
+
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -50,32 +53,55 @@ __device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
   return ((uint64_t)orderable(__fadd_rn(x, 0.f)) << 32) | (uint32_t)~index;
 }
 
-// EPL elements of the logits type per 16-byte load, widened
-template <typename T>
-struct Logits;
-template <>
-struct Logits<float> {
-  static constexpr int kPerLoad = 4;
-  static __device__ __forceinline__ void widen(const uint4& u, float* f) {
-    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
-  }
-  static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
-};
+// A 16-byte load of logits: kPerLoad of them, kept packed in registers (a tile of
+// 64 16-bit logits a thread is 32 registers, and four CTAs fit an SM).
 template <typename T>
 struct Logits {
   static constexpr int kPerLoad = 8;
-  static __device__ __forceinline__ void widen(const uint4& u, float* f) {
-    Storage<T>::to_f32(u, *reinterpret_cast<float(*)[8]>(f));
+  static __device__ __forceinline__ void widen(const uint4& u, float (&f)[8]) {
+    Storage<T>::to_f32(u, f);
   }
-  static __device__ __forceinline__ float one(const T* p) {
-    return static_cast<float>(*p);
+  static __device__ __forceinline__ float one(const T* p) { return static_cast<float>(*p); }
+  // the largest (NaN ignored), two at a time
+  static __device__ __forceinline__ float largest(const uint4& u) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2,
+                                         __nv_bfloat162>::type;
+    T2 h[4];
+    memcpy(h, &u, sizeof(u));
+    const T2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(static_cast<float>(m.x), static_cast<float>(m.y));
+  }
+  static __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
+    T r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = Storage<T>::from_f32(f[e]);
+    uint4 u;
+    memcpy(&u, r, sizeof(u));
+    return u;
+  }
+};
+template <>
+struct Logits<float> {
+  static constexpr int kPerLoad = 4;
+  static __device__ __forceinline__ void widen(const uint4& u, float (&f)[4]) {
+    memcpy(f, &u, sizeof(u));
+  }
+  static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
+  static __device__ __forceinline__ float largest(const uint4& u) {
+    float f[4];
+    widen(u, f);
+    return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
+  }
+  static __device__ __forceinline__ uint4 narrow(const float (&f)[4]) {
+    uint4 u;
+    memcpy(&u, f, sizeof(u));
+    return u;
   }
 };
 
 // One tile of one row: kBeamThreads threads x LOADS 16-byte loads.
 template <typename T, int LOADS>
-__global__ void __launch_bounds__(kBeamThreads)
+__global__ void __launch_bounds__(kBeamThreads, 4)
     beam_tile_kernel(const T* __restrict__ logits, int64_t row_stride, int vocab, int select,
                      int tiles, float* __restrict__ tile_max, float* __restrict__ tile_sum,
                      uint64_t* __restrict__ tile_keys) {
@@ -84,7 +110,7 @@ __global__ void __launch_bounds__(kBeamThreads)
   constexpr int EPL = Logits<T>::kPerLoad;
   constexpr int kPer = EPL * LOADS;
   constexpr int kWarps = kBeamThreads / 32;
-  __shared__ uint32_t group_max[kGroups];
+  __shared__ __align__(16) uint32_t group_max[kGroups];
   __shared__ float warp_max[kWarps], warp_sum[kWarps];
   __shared__ uint64_t cand[kTileCap];
   __shared__ uint32_t threshold;
@@ -95,23 +121,30 @@ __global__ void __launch_bounds__(kBeamThreads)
   const int base = tile * kBeamThreads * kPer;
   // element e of load i of this thread: index base + (i * kBeamThreads + thread) EPL + e;
   // past the row: -inf, which is never a candidate and adds nothing
-  float f[kPer];
+  uint4 u[LOADS];
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
     const int at = base + (i * kBeamThreads + (int)threadIdx.x) * EPL;
     if (at + EPL <= vocab) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + at));
-      Logits<T>::widen(u, f + i * EPL);
+      u[i] = __ldg(reinterpret_cast<const uint4*>(x + at));
     } else {
+      float f[EPL];
 #pragma unroll
-      for (int e = 0; e < EPL; ++e)
-        f[i * EPL + e] = at + e < vocab ? Logits<T>::one(x + at + e) : -INFINITY;
+      for (int e = 0; e < EPL; ++e) f[e] = at + e < vocab ? Logits<T>::one(x + at + e) : -INFINITY;
+      u[i] = Logits<T>::narrow(f);
     }
   }
-  if (threadIdx.x == 0) count = 0;
+  if (threadIdx.x == 0) {
+    count = 0;
+    threshold = 0;
+  }
+  float load_max[LOADS];
   float mx = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) mx = fmaxf(mx, f[i]);
+  for (int i = 0; i < LOADS; ++i) {
+    load_max[i] = Logits<T>::largest(u[i]);
+    mx = fmaxf(mx, load_max[i]);
+  }
   // groups of four neighbouring lanes
   float gm = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
@@ -121,26 +154,29 @@ __global__ void __launch_bounds__(kBeamThreads)
   for (int mask = 4; mask <= 16; mask <<= 1)
     wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, mask));
   __syncthreads();
-  if (warp == 0) {
+  if (threadIdx.x < kGroups) {
     // the select-th largest of the groups' maxima: the largest value with at least
     // `select` maxima at or above it
-    const uint32_t a = group_max[lane], b = group_max[lane + 32];
-    int ra = 0, rb = 0;
+    const uint32_t a = group_max[threadIdx.x];
+    int rank = 0;
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const uint32_t v = group_max[i];
-      ra += v >= a;
-      rb += v >= b;
+    for (int i = 0; i < kGroups; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(group_max + i);
+      rank += (v.x >= a) + (v.y >= a) + (v.z >= a) + (v.w >= a);
     }
-    uint32_t best = max(ra >= select ? a : 0u, rb >= select ? b : 0u);
-    best = __reduce_max_sync(0xffffffffu, best);
-    if (lane == 0) threshold = best;
+    const uint32_t best = __reduce_max_sync(0xffffffffu, rank >= select ? a : 0u);
+    if (lane == 0) atomicMax(&threshold, best);
   }
   // sum of exponentials relative to the warp's maximum; a NaN makes it NaN
   const float ref = wm == -INFINITY ? 0.f : wm;
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) sum += __expf(f[i] - ref);
+  for (int i = 0; i < LOADS; ++i) {
+    float f[EPL];
+    Logits<T>::widen(u[i], f);
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) sum += fast_exp2((f[e] - ref) * 1.4426950408889634f);
+  }
 #pragma unroll
   for (int mask = 1; mask <= 16; mask <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mask);
   if (lane == 0) {
@@ -149,13 +185,22 @@ __global__ void __launch_bounds__(kBeamThreads)
   }
   __syncthreads();
   const float lowest = from_orderable(threshold);
-  if (mx >= lowest) {
+  // The few loads that hold candidates are read again (they are in L2): a loop over
+  // them is a fraction of the code that 64 tests in registers unroll to, and the
+  // instruction cache is what such code waits for.
+  uint32_t hits = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (f[i] >= lowest && f[i] > -INFINITY) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kTileCap)
-          cand[at] = make_key(f[i], base + ((i / EPL) * kBeamThreads + threadIdx.x) * EPL + i % EPL);
+  for (int i = 0; i < LOADS; ++i) hits |= (load_max[i] >= lowest ? 1u : 0u) << i;
+  while (hits) {
+    const int i = __ffs(hits) - 1;
+    hits &= hits - 1;
+    const int at = base + (i * kBeamThreads + (int)threadIdx.x) * EPL;
+#pragma unroll 1
+    for (int e = 0; e < EPL && at + e < vocab; ++e) {
+      const float f = Logits<T>::one(x + at + e);
+      if (f >= lowest && f > -INFINITY) {
+        const int c = atomicAdd(&count, 1);
+        if (c < kTileCap) cand[c] = make_key(f, at + e);
       }
     }
   }
@@ -167,7 +212,7 @@ __global__ void __launch_bounds__(kBeamThreads)
     float S = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      S += warp_sum[w] * (warp_max[w] == -INFINITY ? 1.f : __expf(warp_max[w] - M));
+      S += warp_sum[w] * (warp_max[w] == -INFINITY ? 1.f : expf(warp_max[w] - M));
     tile_max[out] = M;
     tile_sum[out] = S;
   }
@@ -187,13 +232,14 @@ __global__ void __launch_bounds__(kBeamThreads)
   // more ties than the buffer holds: one at a time, each the largest below the last
   uint64_t last = ~0ull;
   uint64_t* best = cand;  // [kWarps]
+  const int end = min(vocab, base + kBeamThreads * kPer);
   for (int r = 0; r < select; ++r) {
     uint64_t k = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint64_t c =
-          make_key(f[i], base + ((i / EPL) * kBeamThreads + threadIdx.x) * EPL + i % EPL);
-      if (f[i] > -INFINITY && c < last && c > k) k = c;
+#pragma unroll 4
+    for (int at = base + (int)threadIdx.x; at < end; at += kBeamThreads) {
+      const float f = Logits<T>::one(x + at);
+      const uint64_t c = make_key(f, at);
+      if (f > -INFINITY && c < last && c > k) k = c;
     }
 #pragma unroll
     for (int mask = 16; mask > 0; mask >>= 1) {
@@ -229,10 +275,20 @@ __global__ void __launch_bounds__(kMergeThreads)
   __shared__ double cs[kMergeCap];
   __shared__ int64_t cf[kMergeCap];
   __shared__ double group_max[kGroups];
-  __shared__ double threshold;
+  __shared__ double half_best[kGroups / 32];
   __shared__ int count;
   const int b = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_beam = tiles * select;
+  const int total = beams * per_beam;
+  // this thread's first candidates, on their way while the rows' sums are added up
+  constexpr int kAhead = 4;
+  uint64_t ahead[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int i = threadIdx.x + j * kMergeThreads;
+    ahead[j] = i < total ? tile_keys[(size_t)b * total + i] : 0;
+  }
   for (int k = warp; k < beams; k += kWarps) {
     const size_t row = (size_t)b * beams + k;
     float M = -INFINITY;
@@ -259,11 +315,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
   if (threadIdx.x == 0) count = 0;
   __syncthreads();
-  const int per_beam = tiles * select;
-  const int total = beams * per_beam;
-  auto score_of = [&](int i, double& s, int64_t& f) {
+  auto score_key = [&](int i, uint64_t key, double& s, int64_t& f) {
     const int k = i / per_beam;
-    const uint64_t key = tile_keys[(size_t)b * total + i];
     s = -INFINITY;
     f = INT64_MAX;
     if (key != 0 && offset[k] > -INFINITY) {
@@ -271,40 +324,48 @@ __global__ void __launch_bounds__(kMergeThreads)
       f = (int64_t)k * vocab + (uint32_t)~(uint32_t)key;
     }
   };
+  auto score_of = [&](int i, double& s, int64_t& f) {
+    score_key(i, tile_keys[(size_t)b * total + i], s, f);
+  };
   // as in a tile: the select-th largest of 64 groups' maxima bounds the result from below
   double top = -INFINITY;
-  for (int i = threadIdx.x; i < total; i += kMergeThreads) {
+  double as[kAhead];
+  int64_t af[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    as[j] = -INFINITY;
+    const int i = threadIdx.x + j * kMergeThreads;
+    if (i < total) score_key(i, ahead[j], as[j], af[j]);
+    top = as[j] > top ? as[j] : top;
+  }
+  for (int i = threadIdx.x + kAhead * kMergeThreads; i < total; i += kMergeThreads) {
     double s;
     int64_t f;
     score_of(i, s, f);
-    top = fmax(top, s);
+    top = s > top ? s : top;
   }
   constexpr int kGroupLanes = kMergeThreads / kGroups;
 #pragma unroll
   for (int mask = 1; mask < kGroupLanes; mask <<= 1)
-    top = fmax(top, __shfl_xor_sync(0xffffffffu, top, mask));
+    top = fmax(top, __shfl_xor_sync(0xffffffffu, top, mask));  // (never NaN)
   if (threadIdx.x % kGroupLanes == 0) group_max[threadIdx.x / kGroupLanes] = top;
   __syncthreads();
-  if (warp == 0) {
-    const double p = group_max[lane], q = group_max[lane + 32];
-    int rp = 0, rq = 0;
-#pragma unroll 8
-    for (int i = 0; i < kGroups; ++i) {
-      rp += group_max[i] >= p;
-      rq += group_max[i] >= q;
-    }
-    double best = fmax(rp >= select ? p : -INFINITY, rq >= select ? q : -INFINITY);
+  if (threadIdx.x < kGroups) {
+    const double p = group_max[threadIdx.x];
+    int rank = 0;
+#pragma unroll 16
+    for (int i = 0; i < kGroups; ++i) rank += group_max[i] >= p;
+    double best = rank >= select ? p : -INFINITY;
 #pragma unroll
-    for (int mask = 16; mask > 0; mask >>= 1)
-      best = fmax(best, __shfl_xor_sync(0xffffffffu, best, mask));
-    if (lane == 0) threshold = best;
+    for (int mask = 16; mask > 0; mask >>= 1) {
+      const double o = __shfl_xor_sync(0xffffffffu, best, mask);
+      best = o > best ? o : best;
+    }
+    if (lane == 0) half_best[warp] = best;
   }
   __syncthreads();
-  const double lowest = threshold;
-  for (int i = threadIdx.x; i < total; i += kMergeThreads) {
-    double s;
-    int64_t f;
-    score_of(i, s, f);
+  const double lowest = half_best[0] > half_best[1] ? half_best[0] : half_best[1];
+  auto collect = [&](double s, int64_t f) {
     if (s > -INFINITY && s >= lowest) {
       const int at = atomicAdd(&count, 1);
       if (at < kMergeCap) {
@@ -312,6 +373,14 @@ __global__ void __launch_bounds__(kMergeThreads)
         cf[at] = f;
       }
     }
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) collect(as[j], af[j]);
+  for (int i = threadIdx.x + kAhead * kMergeThreads; i < total; i += kMergeThreads) {
+    double s;
+    int64_t f;
+    score_of(i, s, f);
+    collect(s, f);
   }
   __syncthreads();
   const int n = count;

@@ -198,6 +198,13 @@ __device__ __forceinline__ float lazy_reference(float& m, float bmax, float& alp
   return mref;
 }
 
+// 2^x by the hardware's approximation (2^-22 relative), results below 2^-126 as 0.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // gpu-scope fetch-and-add with acquire + release semantics.
 __device__ __forceinline__ int atom_add_acq_rel_gpu(int* addr, int v) {
   int old;
