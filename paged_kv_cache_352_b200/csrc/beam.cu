@@ -47,6 +47,19 @@ __device__ __forceinline__ float from_orderable(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
+// Exponentials in base 2: e^x as 2^(x kLog2e - c), with c = fl(ref kLog2e) for a reference
+// ref close to the largest x, so that a term costs one FMA and one ex2. kLog2e is the float
+// below log2 e; what it lacks, kLog2eRest, matters where x is large and acts there like
+// a shift of the reference: sum e^x = 2^(c + ref kLog2eRest) sum 2^(x kLog2e - c) up to
+// |x - ref| kLog2eRest, 2^-25 of a term's exponent.
+constexpr float kLog2e = 1.44269502162933349609375f;
+constexpr double kLog2eRest = 1.9259629911266175e-8;  // log2 e - kLog2e
+constexpr double kLn2 = 0.69314718055994530942;
+
+__device__ __forceinline__ double base2_reference(float ref) {
+  return (double)__fmul_rn(ref, kLog2e) + (double)ref * kLog2eRest;
+}
+
 // (value, index) as one key: larger is better, ties to the smaller index. 0 is
 // below every candidate. -0 counts as 0.
 __device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
@@ -121,19 +134,16 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
   const int base = tile * kBeamThreads * kPer;
   // element e of load i of this thread: index base + (i * kBeamThreads + thread) EPL + e;
   // past the row: -inf, which is never a candidate and adds nothing
+  auto load = [&](int at) {
+    if (at + EPL <= vocab) return __ldg(reinterpret_cast<const uint4*>(x + at));
+    float f[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) f[e] = at + e < vocab ? Logits<T>::one(x + at + e) : -INFINITY;
+    return Logits<T>::narrow(f);
+  };
   uint4 u[LOADS];
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    const int at = base + (i * kBeamThreads + (int)threadIdx.x) * EPL;
-    if (at + EPL <= vocab) {
-      u[i] = __ldg(reinterpret_cast<const uint4*>(x + at));
-    } else {
-      float f[EPL];
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) f[e] = at + e < vocab ? Logits<T>::one(x + at + e) : -INFINITY;
-      u[i] = Logits<T>::narrow(f);
-    }
-  }
+  for (int i = 0; i < LOADS; ++i) u[i] = load(base + (i * kBeamThreads + (int)threadIdx.x) * EPL);
   if (threadIdx.x == 0) {
     count = 0;
     threshold = 0;
@@ -154,29 +164,37 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
   for (int mask = 4; mask <= 16; mask <<= 1)
     wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, mask));
   __syncthreads();
-  if (threadIdx.x < kGroups) {
+  {
     // the select-th largest of the groups' maxima: the largest value with at least
-    // `select` maxima at or above it
-    const uint32_t a = group_max[threadIdx.x];
+    // `select` maxima at or above it; four threads count for each group
+    const uint32_t a = group_max[threadIdx.x >> 2];
     int rank = 0;
 #pragma unroll
-    for (int i = 0; i < kGroups; i += 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(group_max + i);
+    for (int i = 0; i < kGroups / 4; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(group_max + 4 * i + 4 * (lane & 3));
       rank += (v.x >= a) + (v.y >= a) + (v.z >= a) + (v.w >= a);
     }
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
     const uint32_t best = __reduce_max_sync(0xffffffffu, rank >= select ? a : 0u);
     if (lane == 0) atomicMax(&threshold, best);
   }
   // sum of exponentials relative to the warp's maximum; a NaN makes it NaN
   const float ref = wm == -INFINITY ? 0.f : wm;
-  float sum = 0.f;
+  const float minus_c = -__fmul_rn(ref, kLog2e);
+  float even = 0.f, odd = 0.f;  // summed in pairs by packed fp32 instructions
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
     float f[EPL];
     Logits<T>::widen(u[i], f);
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) sum += fast_exp2((f[e] - ref) * 1.4426950408889634f);
+    for (int e = 0; e < EPL; e += 2) {
+      float a = minus_c, b = minus_c;
+      ffma2(a, b, f[e], f[e + 1], kLog2e, kLog2e);
+      fadd2(even, odd, fast_exp2(a), fast_exp2(b));
+    }
   }
+  float sum = even + odd;
 #pragma unroll
   for (int mask = 1; mask <= 16; mask <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mask);
   if (lane == 0) {
@@ -191,18 +209,23 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
   uint32_t hits = 0;
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) hits |= (load_max[i] >= lowest ? 1u : 0u) << i;
+#pragma unroll 1
   while (hits) {
     const int i = __ffs(hits) - 1;
     hits &= hits - 1;
     const int at = base + (i * kBeamThreads + (int)threadIdx.x) * EPL;
-#pragma unroll 1
-    for (int e = 0; e < EPL && at + e < vocab; ++e) {
-      const float f = Logits<T>::one(x + at + e);
-      if (f >= lowest && f > -INFINITY) {
-        const int c = atomicAdd(&count, 1);
-        if (c < kTileCap) cand[c] = make_key(f, at + e);
+    float f[EPL];
+    Logits<T>::widen(load(at), f);
+    uint32_t in = 0;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) in |= (f[e] >= lowest && f[e] > -INFINITY ? 1u : 0u) << e;
+    int c = in ? atomicAdd(&count, __popc(in)) : 0;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e)
+      if ((in >> e) & 1u) {
+        if (c < kTileCap) cand[c] = make_key(f[e], at + e);
+        ++c;
       }
-    }
   }
   const size_t out = (size_t)row * tiles + tile;
   if (threadIdx.x == 0) {
@@ -212,7 +235,9 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
     float S = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      S += warp_sum[w] * (warp_max[w] == -INFINITY ? 1.f : expf(warp_max[w] - M));
+      S += warp_sum[w] * (warp_max[w] == -INFINITY
+                              ? 1.f
+                              : exp2f(__fmul_rn(warp_max[w], kLog2e) - __fmul_rn(M, kLog2e)));
     tile_max[out] = M;
     tile_sum[out] = S;
   }
@@ -275,7 +300,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   __shared__ double cs[kMergeCap];
   __shared__ int64_t cf[kMergeCap];
   __shared__ double group_max[kGroups];
-  __shared__ double half_best[kGroups / 32];
+  __shared__ double warp_best[kWarps];
   __shared__ int count;
   const int b = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -298,14 +323,14 @@ __global__ void __launch_bounds__(kMergeThreads)
     double S = 0.0;
     for (int t = lane; t < tiles; t += 32) {
       const float m = tile_max[row * tiles + t], s = tile_sum[row * tiles + t];
-      if (m > -INFINITY || s != s) S += (double)s * exp((double)m - (double)M);
+      if (m > -INFINITY || s != s) S += (double)s * exp2(base2_reference(m) - base2_reference(M));
     }
 #pragma unroll
     for (int mask = 16; mask > 0; mask >>= 1) S += __shfl_xor_sync(0xffffffffu, S, mask);
     if (lane == 0) {
       const float beam = beam_scores[row];
       double o = -INFINITY;
-      if (M > -INFINITY || S != S) o = (double)beam - ((double)M + log(S));
+      if (M > -INFINITY || S != S) o = (double)beam - kLn2 * (base2_reference(M) + log2(S));
       if (o != o || o == INFINITY) {  // a NaN or +inf among the logits, or as beam score
         report(dev_error, PA_DEVERR_LOGITS);
         o = -INFINITY;
@@ -350,21 +375,28 @@ __global__ void __launch_bounds__(kMergeThreads)
     top = fmax(top, __shfl_xor_sync(0xffffffffu, top, mask));  // (never NaN)
   if (threadIdx.x % kGroupLanes == 0) group_max[threadIdx.x / kGroupLanes] = top;
   __syncthreads();
-  if (threadIdx.x < kGroups) {
-    const double p = group_max[threadIdx.x];
+  {
+    // kGroupLanes threads count for each group
+    const double p = group_max[threadIdx.x / kGroupLanes];
     int rank = 0;
-#pragma unroll 16
-    for (int i = 0; i < kGroups; ++i) rank += group_max[i] >= p;
+#pragma unroll
+    for (int i = 0; i < kGroups / kGroupLanes; ++i)
+      rank += group_max[i * kGroupLanes + threadIdx.x % kGroupLanes] >= p;
+#pragma unroll
+    for (int mask = 1; mask < kGroupLanes; mask <<= 1)
+      rank += __shfl_xor_sync(0xffffffffu, rank, mask);
     double best = rank >= select ? p : -INFINITY;
 #pragma unroll
-    for (int mask = 16; mask > 0; mask >>= 1) {
+    for (int mask = 16; mask >= kGroupLanes; mask >>= 1) {
       const double o = __shfl_xor_sync(0xffffffffu, best, mask);
       best = o > best ? o : best;
     }
-    if (lane == 0) half_best[warp] = best;
+    if (lane == 0) warp_best[warp] = best;
   }
   __syncthreads();
-  const double lowest = half_best[0] > half_best[1] ? half_best[0] : half_best[1];
+  double lowest = warp_best[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) lowest = warp_best[w] > lowest ? warp_best[w] : lowest;
   auto collect = [&](double s, int64_t f) {
     if (s > -INFINITY && s >= lowest) {
       const int at = atomicAdd(&count, 1);

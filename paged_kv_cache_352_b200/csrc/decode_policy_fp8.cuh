@@ -474,17 +474,6 @@ struct Fp8TensorPairPolicy : Fp8TensorPolicy<T, D, G> {
 // CUDA cores over an E4M3 cache
 // ---------------------------------------------------------------------------
 
-// (d0, d1) = (a0 * b0 + d0, a1 * b1 + d1): sm_100's packed fp32 FMA, each half
-// rounded exactly as a scalar fmaf.
-__device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b0,
-                                      float b1) {
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rd, {%0, %1};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rd;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "+f"(d0), "+f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
 // (d0, d1) *= (a, a) with sm_100's packed fp32 multiply.
 __device__ __forceinline__ void fmul2(float& d0, float& d1, float a) {
   asm("{\n\t.reg .b64 ra, rd;\n\t"
