@@ -375,8 +375,10 @@ int pa_rope_table(float* cos_sin, int num_positions, int rotary_dim, double thet
  *   num_select    1 .. PA_BEAM_MAX (2 * beams leave as many after ended ones)
  *   vocab         1 .. 2^24
  *   workspace     device scratch of pa_beam_select_workspace_size() bytes, 256-byte
- *                 aligned; needs no initial value. Calls that run concurrently
- *                 need separate workspaces
+ *                 aligned, ZERO-FILLED before its first use; every completed call
+ *                 leaves its counters zero again, so that it can be reused, also
+ *                 for other sizes that fit. Calls that run concurrently need
+ *                 separate workspaces
  *   dev_error     device int or NULL
  * The outputs must not overlap the inputs. num_seqs == 0 is a no-op. After it,
  * pa_bm_reorder makes the sequences continue their parents.

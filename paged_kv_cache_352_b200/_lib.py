@@ -673,11 +673,11 @@ def pa_beam_select_workspace_size(num_seqs, num_beams, vocab, num_select, dtype=
 
 
 def beam_workspace(num_seqs, num_beams, vocab, num_select, device=None):
-    """A workspace tensor large enough for ``pa_beam_select`` over logits of any type."""
+    """A zero-filled workspace tensor large enough for ``pa_beam_select`` over logits of any type."""
     torch = _torch()
     n = max(pa_beam_select_workspace_size(num_seqs, num_beams, vocab, num_select, code)
             for code in (PA_F16, PA_F32))
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
 def pa_beam_select(scores, parents, tokens, logits, beam_scores, workspace, dev_error=None,

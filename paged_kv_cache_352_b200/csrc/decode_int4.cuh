@@ -74,19 +74,6 @@ constexpr int kInt4Warps = 4;
 constexpr int kInt4Stages = 3;
 constexpr int kInt4CtasPerSm = 4;  // 128 registers a thread
 
-// Copies BYTES (8 or 16) from global to shared memory (a 32-bit shared address)
-// asynchronously.
-template <int BYTES, int DST_OFF = 0, int SRC_OFF = 0>
-__device__ __forceinline__ void cp_async(uint32_t smem, const void* gmem) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(smem), "l"(gmem),
-                 "n"(DST_OFF), "n"(SRC_OFF)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0 + %2], [%1 + %3], 8;" ::"r"(smem), "l"(gmem),
-                 "n"(DST_OFF), "n"(SRC_OFF)
-                 : "memory");
-}
 // A lane's four chunks of a block's codes: two of K, two of V.
 template <int CB>
 __device__ __forceinline__ void copy_block(uint32_t dst, const unsigned char* k,
@@ -96,14 +83,6 @@ __device__ __forceinline__ void copy_block(uint32_t dst, const unsigned char* k,
   cp_async<CB, 64 * CB>(dst, v);
   cp_async<CB, 96 * CB, 32 * CB>(dst, v);
 }
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // d += A B, m16n8k16, half operands, fp32 sums
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {

@@ -93,6 +93,27 @@ __device__ __forceinline__ void bulk_copy_g2s(void* smem_dst, const void* gmem_s
       : "memory");
 }
 
+// Copies BYTES (8 or 16) from global to shared memory (a 32-bit shared address)
+// asynchronously.
+template <int BYTES, int DST_OFF = 0, int SRC_OFF = 0>
+__device__ __forceinline__ void cp_async(uint32_t smem, const void* gmem) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(smem), "l"(gmem),
+                 "n"(DST_OFF), "n"(SRC_OFF)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0 + %2], [%1 + %3], 8;" ::"r"(smem), "l"(gmem),
+                 "n"(DST_OFF), "n"(SRC_OFF)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---- 16-bit storage <-> fp32 -------------------------------------------------
 
 template <typename T>

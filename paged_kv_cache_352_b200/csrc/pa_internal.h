@@ -196,7 +196,8 @@ struct BeamArgs {
   void* workspace;
   int* dev_error;
 };
-// Workspace: per (row, tile) a maximum, a sum of exponentials and `select` keys.
+// Workspace: counters of sequences, then per (row, tile) a maximum, a sum of
+// exponentials and `select` keys.
 struct BeamLayout {
   bool large;  // tile size
   int tiles;   // tiles per row

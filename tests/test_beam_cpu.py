@@ -55,12 +55,12 @@ def test_selection_refusals():
 
 def test_workspace_size():
     n = pa.pa_beam_select_workspace_size
-    assert n(0, 4, 1000, 8) == 0
-    assert n(1, 1, 1, 1) <= 3 * 256
+    base = n(0, 4, 1000, 8)                   # counters
+    assert base <= 2048 and n(1, 1, 1, 1) <= base + 3 * 256   # maxima, sums, keys
     # per (row, tile): a maximum, a sum and `select` 8-byte keys; tiles of at least 2048 logits
     for b, k, v, s in ((1, 4, 32000, 8), (64, 8, 131072, 16), (7, 3, 50257, 64)):
         tiles = -(-v // 2048)
-        assert 0 < n(b, k, v, s) <= b * k * tiles * (8 + 8 * s) + 3 * 256
+        assert 0 < n(b, k, v, s) <= b * k * tiles * (8 + 8 * s) + base + 3 * 256
     with pytest.raises(pa.PAError):
         n(1, 65, 10, 1)
     assert L.lib().pa_beam_select_workspace_size(1, 1, 1, 1, L.PA_F32, None) == L.PA_ERR_INVALID_ARG

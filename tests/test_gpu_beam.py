@@ -159,7 +159,6 @@ def test_padded_rows_stream_graph_and_two_calls_at_once():
         xk = x.clone() if k == 0 else x.flip(0).contiguous()
         sk = s if k == 0 else s.flip(0).flip(1).contiguous()
         ws = pa.beam_workspace(4, 4, 20000, 8)
-        ws.fill_(0xFF)                          # needs no initial value
         out = (torch.zeros(4, 8, device="cuda"),
                torch.zeros(4, 8, dtype=torch.int32, device="cuda"),
                torch.zeros(4, 8, dtype=torch.int32, device="cuda"))
@@ -175,6 +174,14 @@ def test_padded_rows_stream_graph_and_two_calls_at_once():
     for a, b in zip(graphs[0][4], want):
         assert torch.equal(a, b)
     check(graphs[1][4], graphs[1][1], graphs[1][2], 8)
+
+
+def test_one_workspace_for_calls_of_other_sizes():
+    ws = pa.beam_workspace(64, 8, 40000, 16)
+    for B, K, V, n in ((1, 1, 100, 1), (64, 8, 40000, 16), (200, 1, 64, 4), (2, 4, 30000, 8),
+                       (290, 1, 10, 2), (1, 64, 5000, 16), (3, 2, 100, 5), (200, 1, 64, 4)):
+        x, s = make(B, K, V, "bf16", B + V)
+        check(run(x, s, n, ws=ws), x, s, n)
 
 
 def test_refusals_on_device_tensors():
