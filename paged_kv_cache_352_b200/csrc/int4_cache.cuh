@@ -52,13 +52,13 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 //   x clamped to +-65504 (the range of the two halves), mx, mn over the row,
 //   scale = half((mx - mn) / 15), mid = half((mx + mn) * 0.5),
 //   inv = scale > 0 ? 1 / scale : 0, code = clamp(rint((x - mid) * inv + 7.5), 0, 15).
+// (Clamping before rint gives the same code, since the bounds are whole numbers.)
 // A row holding a NaN gets NaN parameters (it reads back as NaN) and codes 0.
 template <int LANES>
 __device__ __forceinline__ uint32_t int4_quantize_row(float (&f)[16], uint32_t (&codes)[2]) {
-  float mx = -INFINITY, mn = INFINITY;
+  float mx = f[0], mn = f[0];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    f[e] = min_nan(max_nan(f[e], -65504.f), 65504.f);
+  for (int e = 1; e < 16; ++e) {
     mx = max_nan(mx, f[e]);
     mn = min_nan(mn, f[e]);
   }
@@ -67,19 +67,40 @@ __device__ __forceinline__ uint32_t int4_quantize_row(float (&f)[16], uint32_t (
     mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, mask));
     mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, mask));
   }
+  if (mx > 65504.f || mn < -65504.f) {  // rare: clamp the elements (and a NaN stays one)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] = min_nan(max_nan(f[e], -65504.f), 65504.f);
+    mx = min_nan(mx, 65504.f);
+    mx = max_nan(mx, -65504.f);
+    mn = max_nan(mn, -65504.f);
+    mn = min_nan(mn, 65504.f);
+  }
   const __half scale = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.f));
   const __half mid = __float2half_rn(__fmul_rn(__fadd_rn(mx, mn), 0.5f));
-  const float s = __half2float(scale), c = __half2float(mid);
+  const float s = __half2float(scale), minus_c = -__half2float(mid);
   const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  // rint by adding 1.5 2^23, whose unit is 1: the code is then the low bits of the float,
+  // under the constant kMagic; the eight of a word join by multiplications by 16, which
+  // move the constants' sum to kRest
+  constexpr uint32_t kMagic = 0x4b400000u;  // 1.5 2^23
+  constexpr uint32_t kRest = kMagic * 0x11111111u;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    codes[h] = 0u;
+    uint32_t w = 0u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float u = __fadd_rn(__fmul_rn(__fsub_rn(f[8 * h + e], c), inv), 7.5f);
-      const int n = min(max(__float2int_rn(u), 0), 15);  // NaN converts to 0
-      codes[h] |= (uint32_t)n << (4 * e);
+    for (int e = 6; e >= 0; e -= 2) {
+      float u = f[8 * h + e], v = f[8 * h + e + 1];
+      fadd2(u, v, minus_c, minus_c);
+      u = __fmul_rn(u, inv);  // (packed multiplications were fused with the next addition)
+      v = __fmul_rn(v, inv);
+      fadd2(u, v, 7.5f, 7.5f);
+      u = fminf(fmaxf(u, 0.f), 15.f);  // NaN: 0
+      v = fminf(fmaxf(v, 0.f), 15.f);
+      fadd2(u, v, 12582912.f, 12582912.f);
+      w = w * 16u + __float_as_uint(v);
+      w = w * 16u + __float_as_uint(u);
     }
+    codes[h] = w - kRest;
   }
   return (uint32_t)__half_as_ushort(scale) | ((uint32_t)__half_as_ushort(mid) << 16);
 }

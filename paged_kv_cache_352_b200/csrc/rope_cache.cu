@@ -53,33 +53,46 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float* f, float scale) {
   return make_uint2(w[0], w[1]);
 }
 
-// T: type of q, key, value. C: cache element (T, E4M3 or Int4). `splits` warps
-// share a token's rows (Hq query, Hkv key, Hkv value rows, in this order).
+// The pair (a, b) turned by an angle's (c, s); every operation rounded by itself.
+__device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
+// T: type of q, key, value. C: cache element (T, E4M3 or Int4). A warp serves two
+// neighbouring tokens: half of its d/16-lane groups the even one, half the odd one.
+// `splits` warps share their rows (Hq query, Hkv key, Hkv value rows, in this order).
+// Two tokens because of the 4-bit value tiles, which interleave the bytes of a slot
+// pair: when the two tokens fill such a pair, as a prompt's do, their lanes exchange
+// halves and each stores 8 bytes where one token alone would store 2 bytes in four
+// places (4096 tokens of 8 heads: 15.4 -> PAIRED us).
 template <typename T, typename C, int D>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_and_cache_kernel(const RopeArgs r, int splits, int rows_per_warp) {
   grid_dependency_wait();
   allow_dependents();
-  constexpr int LANES = D / 16;       // lanes of a row
-  constexpr int RPW = 32 / LANES;     // rows a warp handles at a time
+  constexpr int LANES = D / 16;        // lanes of a row
+  constexpr int RPW = 32 / LANES / 2;  // rows of each token a warp handles at a time
   const int64_t warp = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int u = lane % LANES, sub = lane / LANES;
-  const int64_t t = warp / splits;
-  if (t >= r.num_tokens) return;
-  const int split = (int)(warp - t * splits);
+  const int64_t pair = warp / splits;
+  if (2 * pair >= r.num_tokens) return;
+  const int split = (int)(warp - pair * splits);
   const int rows = r.num_q_heads + 2 * r.num_kv_heads;
   const int row_begin = split * rows_per_warp;
   const int row_end = min(rows, row_begin + rows_per_warp);
+  const int64_t t = 2 * pair + (sub & 1);
+  const bool first_lane = split == 0 && u == 0 && sub < 2;  // of its token, to report
 
-  const int64_t slot = __ldg(r.slot_mapping + t);
-  bool store = slot >= 0;
+  bool live = t < r.num_tokens;  // whether anything of this lane's token is written
+  const int64_t slot = live ? __ldg(r.slot_mapping + t) : -1;
+  bool store = slot >= 0;  // whether its rows are cached
   if (slot >= r.num_slots) {
     store = false;
-    if (lane == 0 && split == 0) report(r.dev_error, PA_DEVERR_SLOT_RANGE);
+    if (first_lane) report(r.dev_error, PA_DEVERR_SLOT_RANGE);
   }
-  const int64_t block = store ? slot / kBlockSize : 0;
-  const int tok = store ? (int)(slot - block * kBlockSize) : 0;
 
   const bool rot = u < r.rotary_dim / 16;
   float cs[8], sn[8];
@@ -88,13 +101,12 @@ __global__ void __launch_bounds__(kRopeThreads)
     cs[e] = 1.f;
     sn[e] = 0.f;
   }
-  if (r.rotary_dim > 0) {
+  if (r.rotary_dim > 0 && live) {
     const int64_t p = __ldg(r.positions + t);
     if (p < 0 || p >= r.num_positions) {  // nothing of this token is written
-      if (lane == 0 && split == 0) report(r.dev_error, PA_DEVERR_POSITION);
-      return;
-    }
-    if (rot) {
+      if (first_lane) report(r.dev_error, PA_DEVERR_POSITION);
+      live = store = false;
+    } else if (rot) {
       const float* row = r.cos_sin + p * r.rotary_dim + 8 * u;
       const float4 c0 = __ldg(reinterpret_cast<const float4*>(row));
       const float4 c1 = __ldg(reinterpret_cast<const float4*>(row) + 1);
@@ -106,6 +118,14 @@ __global__ void __launch_bounds__(kRopeThreads)
       sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
     }
   }
+  const int64_t block = store ? slot / kBlockSize : 0;
+  const int tok = store ? (int)(slot - block * kBlockSize) : 0;
+  // whether the two tokens fill slots 2i and 2i + 1 (of one block, then): uniform
+  bool paired = false;
+  if constexpr (std::is_same<C, Int4>::value) {
+    const int64_t other = __shfl_xor_sync(0xffffffffu, store ? slot : -4, LANES);
+    paired = __all_sync(0xffffffffu, store && (slot ^ 1) == other && (int)(slot & 1) == (sub & 1));
+  }
   const bool halves = rot && !r.interleaved;
   // the lane's chunks of a query or key row; of a value row they are 16u, 16u + 8
   const int off_a = halves ? 8 * u : 16 * u;
@@ -115,9 +135,9 @@ __global__ void __launch_bounds__(kRopeThreads)
     uint4 raw[kUnroll][2];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int row = base + i * RPW + sub;
+      const int row = base + i * RPW + (sub >> 1);
       raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (row >= row_end) continue;
+      if (row >= row_end || !live) continue;
       const T* src;
       int oa = off_a, ob = off_b;
       if (row < r.num_q_heads) {
@@ -141,8 +161,8 @@ __global__ void __launch_bounds__(kRopeThreads)
     for (int i = 0; i < kUnroll; ++i) {
       const int first = base + i * RPW;
       if (first >= row_end) break;  // uniform across the warp
-      const int row = first + sub;
-      const bool in = row < row_end;
+      const int row = first + (sub >> 1);
+      const bool in = live && row < row_end;
       const bool is_q = row < r.num_q_heads;
       const bool is_v = row >= r.num_q_heads + r.num_kv_heads;
       float f[16];
@@ -151,18 +171,10 @@ __global__ void __launch_bounds__(kRopeThreads)
       if (rot && !is_v) {
         if (halves) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float a = f[e], b = f[8 + e];
-            f[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
-            f[8 + e] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
-          }
+          for (int e = 0; e < 8; ++e) rotate(f[e], f[8 + e], cs[e], sn[e]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float a = f[2 * e], b = f[2 * e + 1];
-            f[2 * e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
-            f[2 * e + 1] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
-          }
+          for (int e = 0; e < 8; ++e) rotate(f[2 * e], f[2 * e + 1], cs[e], sn[e]);
         }
       }
       if (in && is_q) {
@@ -178,10 +190,20 @@ __global__ void __launch_bounds__(kRopeThreads)
       if constexpr (std::is_same<C, Int4>::value) {
         uint32_t codes[2];
         const uint32_t par = int4_quantize_row<LANES>(f, codes);
+        // the even token's lane takes the pair's first 8 dimensions, the odd one's the other 8
+        const bool odd = sub & 1;
+        const uint32_t got =
+            __shfl_xor_sync(0xffffffffu, odd ? codes[0] : codes[1], LANES);
         if (write) {
           unsigned char* dst =
               static_cast<unsigned char*>(is_v ? r.v_cache : r.k_cache) + tile * int4_tile_bytes(D);
-          if (is_v) {
+          if (is_v && paired) {
+            const uint32_t even_codes = odd ? got : codes[0], odd_codes = odd ? codes[1] : got;
+            const int x = 16 * u + (odd ? 8 : 0);
+            *reinterpret_cast<uint2*>(dst + int4_value_byte<D>(tok & ~1, x)) =
+                make_uint2(__byte_perm(even_codes, odd_codes, 0x5410),
+                           __byte_perm(even_codes, odd_codes, 0x7632));
+          } else if (is_v) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               *reinterpret_cast<uint16_t*>(dst + int4_value_byte<D>(tok, 16 * u + 4 * q)) =
@@ -270,20 +292,20 @@ __global__ void __launch_bounds__(256)
 
 template <typename T, typename C, int D>
 cudaError_t launch_rope_typed(const RopeArgs& r, cudaStream_t stream) {
-  constexpr int RPW = 32 / (D / 16);
+  constexpr int RPW = 32 / (D / 16) / 2;
   const int rows = r.num_q_heads + 2 * r.num_kv_heads;
   if (r.num_tokens == 0 || rows == 0) return cudaSuccess;
-  // Warps that share a token's rows: one per RPW rows while the tokens alone do
+  // Warps that share a token pair's rows: one per RPW rows while the tokens alone do
   // not give the 148 SMs 16 warps each, fewer as tokens grow (a warp that keeps
-  // a token's rows loads its cos and sin once).
+  // a pair's rows loads its cos and sin once).
   const int groups = (rows + RPW - 1) / RPW;
+  const long long pairs = ((long long)r.num_tokens + 1) / 2;
   const long long target = 148 * 16;
-  long long splits = (target + r.num_tokens - 1) / r.num_tokens;
+  long long splits = (target + pairs - 1) / pairs;
   if (splits > groups) splits = groups;
   const int per = (int)((groups + splits - 1) / splits);
   const int used = (groups + per - 1) / per;
-  const long long warps = (long long)r.num_tokens * used;
-  const long long ctas = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  const long long ctas = (pairs * used + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_dependent(rope_and_cache_kernel<T, C, D>, dim3((unsigned)ctas), dim3(kRopeThreads),
                           0, stream, r, used, per * RPW);
