@@ -32,6 +32,12 @@ __device__ __forceinline__ int int4_value_byte(int t, int x) {
          ((t & 1) << 1) + ((x >> 1) & 1);
 }
 
+// What int4_value_byte grows by from dimensions 16u to 16u + 4q, q < 4.
+template <int D>
+__device__ __forceinline__ constexpr int int4_value_step(int q) {
+  return D == 128 ? 4 * q : 32 * (q >> 1) + 4 * (q & 1);
+}
+
 // min / max that return NaN when an operand is NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;

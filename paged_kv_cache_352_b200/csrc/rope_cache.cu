@@ -16,7 +16,7 @@
 // chunks at 8u and R/2 + 8u, for adjacent pairs 16u and 16u + 8, and in both it
 // needs the table entries 8u .. 8u + 7 of cos and of sin. Those are loaded once
 // per lane and used for every row the lane turns; rows a lane handles are
-// unrolled by kUnroll, whose loads are issued together.
+// unrolled, their loads issued together.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -28,8 +28,21 @@
 namespace pa {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kRopeThreads = 128;
+
+// Rows of each token that a lane group loads at once, and CTAs per SM: four and five
+// (64 bytes a lane in flight, 96 registers) where rows are copied, two and six where
+// quantizing them needs the registers. 16384 tokens of 32 + 8 heads, 16-bit: 73.0 us
+// with 256 threads and no bound, 71.0 us with two and six, 68.9 us so; 4096 tokens into
+// 4 bits: 27.0, 26.3 and 28.4 us.
+template <typename C>
+struct RopeShape {
+  static constexpr int kUnroll = 4, kCtasPerSm = 5;
+};
+template <>
+struct RopeShape<Int4> {
+  static constexpr int kUnroll = 2, kCtasPerSm = 6;
+};
 
 template <typename T>
 __device__ __forceinline__ uint4 from_f32x8(const float* f) {
@@ -66,13 +79,14 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
 // Two tokens because of the 4-bit value tiles, which interleave the bytes of a slot
 // pair: when the two tokens fill such a pair, as a prompt's do, their lanes exchange
 // halves and each stores 8 bytes where one token alone would store 2 bytes in four
-// places (4096 tokens of 8 heads: 15.4 -> PAIRED us).
+// places (4096 tokens of 8 heads: 15.4 -> 10.2 us).
 template <typename T, typename C, int D>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, RopeShape<C>::kCtasPerSm)
     rope_and_cache_kernel(const RopeArgs r, int splits, int rows_per_warp) {
   grid_dependency_wait();
   allow_dependents();
   constexpr int LANES = D / 16;        // lanes of a row
+  constexpr int kUnroll = RopeShape<C>::kUnroll;
   constexpr int RPW = 32 / LANES / 2;  // rows of each token a warp handles at a time
   const int64_t warp = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -126,6 +140,12 @@ __global__ void __launch_bounds__(kRopeThreads)
     const int64_t other = __shfl_xor_sync(0xffffffffu, store ? slot : -4, LANES);
     paired = __all_sync(0xffffffffu, store && (slot ^ 1) == other && (int)(slot & 1) == (sub & 1));
   }
+  // places inside a 4-bit tile: this token's key row, its values' first two bytes, and the
+  // 8 bytes of the pair that this lane stores when both tokens are there
+  const int odd8 = (sub & 1) ? 8 : 0;
+  const int k_place = tok * (D / 2);
+  const int v_place = int4_value_byte<D>(tok, 16 * u);
+  const int pair_place = int4_value_byte<D>(tok & ~1, 16 * u + odd8);
   const bool halves = rot && !r.interleaved;
   // the lane's chunks of a query or key row; of a value row they are 16u, 16u + 8
   const int off_a = halves ? 8 * u : 16 * u;
@@ -192,25 +212,23 @@ __global__ void __launch_bounds__(kRopeThreads)
         const uint32_t par = int4_quantize_row<LANES>(f, codes);
         // the even token's lane takes the pair's first 8 dimensions, the odd one's the other 8
         const bool odd = sub & 1;
-        const uint32_t got =
-            __shfl_xor_sync(0xffffffffu, odd ? codes[0] : codes[1], LANES);
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? codes[0] : codes[1], LANES);
         if (write) {
           unsigned char* dst =
               static_cast<unsigned char*>(is_v ? r.v_cache : r.k_cache) + tile * int4_tile_bytes(D);
           if (is_v && paired) {
             const uint32_t even_codes = odd ? got : codes[0], odd_codes = odd ? codes[1] : got;
-            const int x = 16 * u + (odd ? 8 : 0);
-            *reinterpret_cast<uint2*>(dst + int4_value_byte<D>(tok & ~1, x)) =
+            *reinterpret_cast<uint2*>(dst + pair_place) =
                 make_uint2(__byte_perm(even_codes, odd_codes, 0x5410),
                            __byte_perm(even_codes, odd_codes, 0x7632));
           } else if (is_v) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint16_t*>(dst + int4_value_byte<D>(tok, 16 * u + 4 * q)) =
+              *reinterpret_cast<uint16_t*>(dst + v_place + int4_value_step<D>(q)) =
                   (uint16_t)(codes[q >> 1] >> (16 * (q & 1)));
           } else {
-            *reinterpret_cast<uint32_t*>(dst + tok * (D / 2) + oa / 2) = codes[0];
-            *reinterpret_cast<uint32_t*>(dst + tok * (D / 2) + ob / 2) = codes[1];
+            *reinterpret_cast<uint32_t*>(dst + k_place + oa / 2) = codes[0];
+            *reinterpret_cast<uint32_t*>(dst + k_place + ob / 2) = codes[1];
           }
           if (u == 0) *reinterpret_cast<uint32_t*>(dst + 8 * D + 4 * tok) = par;
         }
@@ -296,11 +314,11 @@ cudaError_t launch_rope_typed(const RopeArgs& r, cudaStream_t stream) {
   const int rows = r.num_q_heads + 2 * r.num_kv_heads;
   if (r.num_tokens == 0 || rows == 0) return cudaSuccess;
   // Warps that share a token pair's rows: one per RPW rows while the tokens alone do
-  // not give the 148 SMs 16 warps each, fewer as tokens grow (a warp that keeps
+  // not give the 148 SMs 64 warps each, fewer as tokens grow (a warp that keeps
   // a pair's rows loads its cos and sin once).
   const int groups = (rows + RPW - 1) / RPW;
   const long long pairs = ((long long)r.num_tokens + 1) / 2;
-  const long long target = 148 * 16;
+  const long long target = 148 * 64;
   long long splits = (target + pairs - 1) / pairs;
   if (splits > groups) splits = groups;
   const int per = (int)((groups + splits - 1) / splits);
