@@ -905,6 +905,12 @@ int pa_sched_attach(pa_sched* s, int num_q_heads, int num_kv_heads, int head_dim
 int pa_sched_attach_fp8(pa_sched* s, int num_q_heads, int num_kv_heads, int head_dim, int dtype,
                         int max_context_len, float k_scale, float v_scale);
 
+/* pa_sched_attach over 4-bit caches: pa_reshape_and_cache_int4, pa_paged_decode_int4
+ * and copies and swaps of PA_INT4 pools (the pinned host pool is [num_host_blocks]
+ * [Hkv][16][head_dim/2 + 4] bytes). Never through the cascade, whatever its mode. */
+int pa_sched_attach_int4(pa_sched* s, int num_q_heads, int num_kv_heads, int head_dim, int dtype,
+                         int max_context_len);
+
 /* Decode of sequences that share leading blocks, inside the executor. Samples
  * forked from one prompt share its full blocks, and so do requests whose
  * prompts were found in the prefix cache ("PagedAttention: The vLLM Paper",

@@ -150,6 +150,7 @@ _SIGS = {
     "pa_sched_attach": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int]),
     "pa_sched_attach_fp8": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, ctypes.c_float,
                                      ctypes.c_float]),
+    "pa_sched_attach_int4": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int]),
     "pa_sched_set_cascade": (_c_int, [_vp, _c_int]),
     "pa_sched_last_cascade": (_c_int, [_vp, ctypes.POINTER(_c_int),
                                        ctypes.POINTER(ctypes.c_int64)]),
@@ -1176,12 +1177,18 @@ class Scheduler:
         }
 
     def attach(self, num_q_heads: int, num_kv_heads: int, head_dim: int, dtype,
-               max_context_len: int, fp8_scales=None) -> None:
+               max_context_len: int, fp8_scales=None, int4=False) -> None:
         """Allocate the executor for queries/inputs of ``dtype``; with
-        ``fp8_scales=(k_scale, v_scale)`` the pools are 8-bit E4M3 caches."""
+        ``fp8_scales=(k_scale, v_scale)`` the pools are 8-bit E4M3 caches, with
+        ``int4`` 4-bit caches."""
         code = dtype if isinstance(dtype, int) else (
             PA_F16 if dtype == _torch().float16 else PA_BF16)
-        if fp8_scales is None:
+        if int4 and fp8_scales is not None:
+            raise PAError(PA_ERR_INVALID_ARG, "fp8_scales and int4 exclude each other")
+        if int4:
+            _check(self._lib.pa_sched_attach_int4(self._h, num_q_heads, num_kv_heads, head_dim,
+                                                  code, max_context_len))
+        elif fp8_scales is None:
             _check(self._lib.pa_sched_attach(self._h, num_q_heads, num_kv_heads, head_dim, code,
                                              max_context_len))
         else:
@@ -1190,6 +1197,7 @@ class Scheduler:
                                                  float(fp8_scales[1])))
         self.io_dtype = code
         self.fp8 = fp8_scales is not None
+        self.int4 = int4
 
     def set_cascade(self, mode: int) -> None:
         """When the executor decodes sequences that share leading blocks through
@@ -1209,7 +1217,9 @@ class Scheduler:
         whose leading dimension covers the plan's counts; host_k/host_v are the
         pinned host pool (or None)."""
         torch = _torch()
-        if (dtype_code(k_cache) == PA_FP8_E4M3) != getattr(self, "fp8", False):
+        code = _pool_dims(k_cache, v_cache)[4]
+        if (code == PA_FP8_E4M3) != getattr(self, "fp8", False) or (
+                code == PA_INT4) != getattr(self, "int4", False):
             raise PAError(PA_ERR_INVALID_ARG, "cache element type differs from the attached one")
         cdt = k_cache.dtype
         dt = q.dtype

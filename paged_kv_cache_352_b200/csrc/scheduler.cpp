@@ -108,7 +108,7 @@ struct pa_sched {
   // executor
   bool attached = false;
   int hq = 0, hkv = 0, head_dim = 0, dtype = 0, max_ctx_cap = 0, max_blocks_cap = 0;
-  int cache_dtype = 0;              // dtype, or PA_FP8_E4M3
+  int cache_dtype = 0;              // dtype, PA_FP8_E4M3 or PA_INT4
   float k_scale = 1.f, v_scale = 1.f;
   size_t cap_prefill = 0, cap_tokens = 0, meta_bytes = 0;
   void* dev_meta = nullptr;
@@ -688,6 +688,14 @@ int pa_sched_attach_fp8(pa_sched* s, int num_q_heads, int num_kv_heads, int head
   return PA_OK;
 }
 
+int pa_sched_attach_int4(pa_sched* s, int num_q_heads, int num_kv_heads, int head_dim, int dtype,
+                         int max_context_len) {
+  if (int st = pa_sched_attach(s, num_q_heads, num_kv_heads, head_dim, dtype, max_context_len))
+    return st;
+  s->cache_dtype = PA_INT4;
+  return PA_OK;
+}
+
 int pa_sched_execute(pa_sched* s, void* k_cache, void* v_cache, void* host_k, void* host_v,
                      const void* prefill_key, const void* prefill_value, const void* key,
                      const void* value, const void* q, void* out, float scale, int* dev_error,
@@ -727,6 +735,7 @@ int pa_sched_execute(pa_sched* s, void* k_cache, void* v_cache, void* host_k, vo
   if (s->cascade_mode == PA_SCHED_CASCADE_AUTO)
     for (int i = 0; i < nseq && !consider; ++i)
       consider = !s->req(p.batch_request[i]).tokens.empty();
+  if (s->cache_dtype == PA_INT4) consider = false;  // the cascade reads 16- and 8-bit caches
   if (consider && s->cascade_ws && nseq >= 2 && gsz >= 2) {
     s->ids_tmp.resize(nseq);
     for (int i = 0; i < nseq; ++i)
@@ -840,7 +849,7 @@ int pa_sched_execute(pa_sched* s, void* k_cache, void* v_cache, void* host_k, vo
 
   const int nh = s->bm->num_host_blocks;
   const int cdt = s->cache_dtype;
-  const bool fp8 = cdt == PA_FP8_E4M3;
+  const bool fp8 = cdt == PA_FP8_E4M3, int4 = cdt == PA_INT4;
   if (!p.swap_out.empty())
     if (int r = pa_swap_blocks(k_cache, v_cache, nb, host_k, host_v, nh, p.swap_out.data(),
                                (int)p.swap_out.size() / 2, hkv, d, bs, cdt, stream))
@@ -853,6 +862,9 @@ int pa_sched_execute(pa_sched* s, void* k_cache, void* v_cache, void* host_k, vo
   // the cache writes of one token list (prefill or new tokens) in the cache's type
   auto write = [&](const void* kk, const void* vv, size_t off_slots, int n) {
     const int64_t* slots = reinterpret_cast<const int64_t*>(dm + off_slots);
+    if (int4)
+      return pa_reshape_and_cache_int4(kk, vv, row, row, k_cache, v_cache, slots, n, hkv, d, bs, nb,
+                                       s->dtype, dev_error, stream);
     return fp8 ? pa_reshape_and_cache_fp8(kk, vv, row, row, k_cache, v_cache, slots, n, hkv, d, bs,
                                           nb, s->dtype, s->k_scale, s->v_scale, dev_error, stream)
                : pa_reshape_and_cache(kk, vv, row, row, k_cache, v_cache, slots, n, hkv, d, bs, nb,
@@ -885,6 +897,10 @@ int pa_sched_execute(pa_sched* s, void* k_cache, void* v_cache, void* host_k, vo
                                            gm, gp, sg, sm, ng, gsz, maxp, s->cascade_ws,
                                            s->cascade_ws_bytes, dev_error, s->dtype, stream);
     }
+    if (int4)
+      return pa_paged_decode_int4(out, q, k_cache, v_cache, tables, p.max_blocks, ctx, order, nseq,
+                                  p.max_ctx, s->hq, hkv, d, bs, nb, scale, 0, s->workspace,
+                                  s->workspace_bytes, dev_error, s->dtype, stream);
     const int r =
         fp8 ? pa_paged_decode_fp8(out, q, k_cache, v_cache, tables, p.max_blocks, ctx, order, nseq,
                                   p.max_ctx, s->hq, hkv, d, bs, nb, scale, s->k_scale, s->v_scale,

@@ -447,6 +447,70 @@ def test_stall_request_is_left_to_the_other_decodes():
     assert err.item() & pa.PA_DEVERR_WAIT_TIMEOUT
 
 
+@pytest.mark.parametrize("mode,host,cascade", [("swap", 400, None), ("recompute", 0, None),
+                                               ("swap", 400, pa.PA_SCHED_CASCADE_ON)])
+def test_serving_loop_over_a_4_bit_cache(mode, host, cascade):
+    """The scheduler's executor attached to 4-bit pools: admissions, copy-on-write, preemption by
+    swap or recomputation, every step's pool bytes and outputs against the oracle; the cascade
+    stays off whatever its mode."""
+    hq, hkv, d, dt, nb, cap = 8, 2, 64, "f16", 18, 10
+    swap = mode == "swap"
+    order = np.random.default_rng(61).permutation(nb)
+    pm = pa.PA_PREEMPT_SWAP if swap else pa.PA_PREEMPT_RECOMPUTE
+    c = pa.Scheduler(nb, 16, order, max_num_seqs=cap, num_host_blocks=host, preempt_mode=pm)
+    rng = np.random.default_rng(62)
+    trace = [(i, int(rng.integers(1, 60)), int(rng.integers(1, 25)),
+              int(rng.integers(1, 4)) if swap else 1, int(rng.integers(0, 6))) for i in range(24)]
+    for t in trace:
+        c.submit(*t)
+    c.attach(hq, hkv, d, torch.float16, 90, int4=True)
+    if cascade is not None:
+        c.set_cascade(cascade)
+    kc, vc = caches(nb, hkv, d, 0)
+    ok, ov = kc.cpu().numpy(), vc.cpu().numpy()
+    hk, hv = (torch.zeros(max(host, 1), hkv, 16, d // 2 + 4, dtype=torch.uint8).pin_memory()
+              for _ in range(2))
+    sk, sv = hk.numpy().copy(), hv.numpy().copy()
+    toks = gen.RequestTokens(63, {t[0]: t[1] for t in trace}, hkv, d, dt,
+                             prompt_tokens={t[0]: None for t in trace})
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    seen = {"swap_out": 0, "swap_in": 0, "copies": 0, "preempted": 0}
+    step = 0
+    while not c.idle():
+        c.step()
+        p = c.plan()
+        for k in seen:
+            seen[k] += len(p[k])
+
+        def rows(ws):
+            got = [toks.row(r, s, pos) for r, s, pos, _ in ws]
+            pick = lambda i: np.array([x[i] for x in got], np.uint16).reshape(-1, hkv, d)
+            return pick(0), pick(1), [int(w[3]) for w in ws]
+
+        pk, pv, ps = rows(p["prefill"])
+        wk, wv, ws = rows(p["writes"])
+        q = gen.normal_bits([64, step], (len(p["batch"]), hq, d), dt)
+        out = torch.empty(len(p["batch"]), hq, d, dtype=torch.float16, device="cuda")
+        c.execute(kc, vc, hk if host else None, hv if host else None, dev16(pk, dt), dev16(pv, dt),
+                  dev16(wk, dt), dev16(wv, dt), dev16(q, dt), out, 0.125, dev_error=err)
+        torch.cuda.synchronize()
+        assert c.last_cascade()[0] == 0
+        for a, b in p["swap_out"]:
+            sk[b], sv[b] = ok[a], ov[a]
+        for a, b in p["swap_in"]:
+            ok[b], ov[b] = sk[a], sv[a]
+        I4.reshape_and_cache_int4(ok, ov, f32(pk, dt), f32(pv, dt), ps)
+        for a, b in p["copies"]:
+            ok[b], ov[b] = ok[a], ov[a]
+        I4.reshape_and_cache_int4(ok, ov, f32(wk, dt), f32(wv, dt), ws)
+        assert np.array_equal(kc.cpu().numpy(), ok) and np.array_equal(vc.cpu().numpy(), ov)
+        ctx = [int(x[2]) for x in p["batch"]]
+        check_decode(out, q, ok, ov, np.asarray(p["tables"]), ctx, 0.125, dt)
+        step += 1
+    assert err.item() == 0 and seen["preempted"] > 0, seen
+    assert not swap or (seen["swap_in"] > 0 and seen["copies"] > 0), seen
+
+
 def test_refusals_on_device_tensors():
     b = Batch([20], 2, 2, 64, "f16", 31)
     with pytest.raises(pa.PAError):                     # an E4M3-shaped pool
