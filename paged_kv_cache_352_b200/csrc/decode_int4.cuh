@@ -45,10 +45,11 @@
 //
 // Precision. Products are exact, sums are fp32. q is brought below 2^15 by a
 // power of two (exact in half unless 2^29 below the row's largest element). The
-// weights w are rounded to half precision relative to the largest value scale
-// seen (a power of two S, raised when a larger scale comes, as the softmax
-// reference is), and 7.5 sum w is taken over the rounded weights, so that their
-// errors multiply the centred codes. For half outputs the rounding residual of
+// weights w are rounded to half precision in units that put the largest at 2^7 when
+// the reference moves; it moves when a weight reaches 2^15, 1/2 of half's range (one
+// test on the packed halves stands for the running maximum of scores and of scales).
+// 7.5 sum w is taken over the rounded weights, so that their errors multiply the
+// centred codes. For half outputs the rounding residual of
 // w joins the product too: with at most 4 query heads per KV head heads repeat
 // in columns 4-7, whose lanes feed the residual (no cost); with 8 it is a second
 // product. For bf16 outputs the weights' 2^-11 is 1/8 of the output's own step.
@@ -91,6 +92,17 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = c + A B: a chain's first product, its start kept in other registers
+__device__ __forceinline__ void mma_16816_from(float (&d)[4], const float (&c)[4], uint32_t a0,
+                                               uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+        "f"(c[3]));
+}
+
 // Transposes an 8 x 8 matrix of halves spread over the warp (row lane / 4).
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t d;
@@ -149,11 +161,12 @@ struct Int4State {
   uint4 qraw[W];
   uint32_t qb[KSTEPS][2];           // head g's operand
   // Of heads 2c, 2c + 1. Everything accumulated is in units of 2^ref: ref is the
-  // softmax reference m plus log2 S - 7, S a power of two at or above every value
-  // scale seen (0 before the first positive one). l and pmid are this lane's share
-  // (tokens g, g + 8).
+  // softmax reference m plus log2 S - 7, S a power of two at or above the largest
+  // value scale when the reference last moved (0 before a positive one). l and pmid
+  // are this lane's share (tokens g, g + 8).
   float m[2], ref[2], l[2], pmid[2], row_scale[2], qsum[2];
-  float vmax;  // S
+  float centre[4];  // -7.5 qsum, where the products of a tile start
+  float vmax;       // S
   float o[MT][4], ow[4];
 
   // the head of column h
@@ -206,8 +219,9 @@ struct Int4State {
     for (int e = 0; e < 2; ++e) {
       qsum[e] = qs[e];
       row_scale[e] = __shfl_sync(0xffffffffu, rs, 8 * c + 4 * e);
-      m[e] = -INFINITY;
-      ref[e] = l[e] = pmid[e] = 0.f;
+      centre[e] = centre[2 + e] = -7.5f * qsum[e];
+      m[e] = ref[e] = -INFINITY;
+      l[e] = pmid[e] = 0.f;
     }
     vmax = 0.f;
 #pragma unroll
@@ -223,32 +237,84 @@ struct Int4State {
     return half2_bits_to_float2(*reinterpret_cast<const uint32_t*>(p + 4 * t));
   }
 
-  // A softmax reference or the value-scale reference S moves: brings what has
-  // accumulated to the new ones (which are the same in every lane of a column).
-  __device__ __forceinline__ void move(float (&bmax)[2], float smax) {
+  // Weights of a step: t the scores over row_scale, in the references' units.
+  struct Weights {
+    float p[2];         // sum of p per head, this lane's tokens
+    float pm[2];        // sum of p mid
+    float w[2][2][2];   // [block][i][e]
+    uint32_t h[2][2];   // the same as halves
+    // Whether a weight leaves the range: some w at or past 2^15 (or inf or NaN, which a
+    // reference of -inf gives too), or p far past what S = its scale would allow.
+    __device__ __forceinline__ bool out_of_range() const {
+      const uint32_t m = __vmaxu2(__vmaxu2(h[0][0], h[0][1]), __vmaxu2(h[1][0], h[1][1]));
+      return ((m + 0x08000800u) & 0x80008000u) != 0u || !(p[0] + p[1] <= 1.15e18f);
+    }
+  };
+
+  template <bool kMask>
+  __device__ __forceinline__ void weigh(const float (&t)[2][4], const float2 (&vp)[2][2],
+                                        int valid0, int valid1, Weights& r) const {
+    r.p[0] = r.p[1] = r.pm[0] = r.pm[1] = 0.f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool in = !kMask || g + 8 * i < (b ? valid1 : valid0);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float z = fmaf(t[b][2 * i + e], row_scale[e], -ref[e]);
+          if (!in) z = -INFINITY;
+          const float p = fast_exp2(z);
+          r.p[e] += p;
+          r.pm[e] = fmaf(p, vp[b][i].y, r.pm[e]);
+          r.w[b][i][e] = p * vp[b][i].x;
+        }
+        const __half2 h = __floats2half2_rn(r.w[b][i][0], r.w[b][i][1]);
+        memcpy(&r.h[b][i], &h, 4);
+      }
+  }
+
+  // Moves the references to cover a step whose weights left the range (the first step
+  // among them), and brings what has accumulated to the new ones, which are the same in
+  // every lane of a column. After it no weight of the step is past 2^7.
+  template <bool kMask>
+  __device__ __forceinline__ void move(const float (&t)[2][4], const float2 (&vp)[2][2],
+                                       int valid0, int valid1) {
+    float bmax[2] = {-INFINITY, -INFINITY};
+    float smax = 0.f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        smax = fmaxf(smax, vp[b][i].x);
+        if (!kMask || g + 8 * i < (b ? valid1 : valid0)) {
+          bmax[0] = fmaxf(bmax[0], t[b][2 * i] * row_scale[0]);
+          bmax[1] = fmaxf(bmax[1], t[b][2 * i + 1] * row_scale[1]);
+        }
+      }
 #pragma unroll
     for (int mask = 4; mask <= 16; mask <<= 1) {
       bmax[0] = fmaxf(bmax[0], __shfl_xor_sync(0xffffffffu, bmax[0], mask));
       bmax[1] = fmaxf(bmax[1], __shfl_xor_sync(0xffffffffu, bmax[1], mask));
       smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, mask));
     }
-    // the power of two at or above smax (a half: exact here)
+    // S: the power of two at or above every scale looked at (a half: exact here)
     if (smax > vmax)
       vmax = __uint_as_float((__float_as_uint(smax) + 0x007fffffu) & 0x7f800000u);
     const float shift = vmax > 0.f ? (float)((int)(__float_as_uint(vmax) >> 23) - 127 - 7) : 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const bool first = m[e] == -INFINITY;  // nothing of this head has accumulated
-      if (bmax[e] > m[e] + kLazyRescaleLog2) m[e] = bmax[e];
+      m[e] = fmaxf(m[e], bmax[e]);
       const float to = (m[e] == -INFINITY ? 0.f : m[e]) + shift;
       const float alpha = first ? 1.f : exp2f(ref[e] - to);
       ref[e] = to;
       l[e] *= alpha;
       pmid[e] *= alpha;
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        o[t][e] *= alpha;
-        o[t][2 + e] *= alpha;
+      for (int i = 0; i < MT; ++i) {
+        o[i][e] *= alpha;
+        o[i][2 + e] *= alpha;
       }
       ow[e] *= alpha;
     }
@@ -260,13 +326,11 @@ struct Int4State {
   template <bool kMask>
   __device__ __forceinline__ void step(const unsigned char* codes, const unsigned char* par,
                                        int valid0, int valid1) {
-    auto in = [&](int b, int i) { return !kMask || g + 8 * i < (b ? valid1 : valid0); };
     // ---- S = K Q^T
-    float x[2][4];  // [block][2 i + e]: token g + 8 i, head 2c + e
+    float t[2][4];  // [block][2 i + e]: token g + 8 i, head 2c + e
+    float2 vp[2][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      x[b][0] = x[b][2] = -7.5f * qsum[0];  // the product starts from the codes' centre
-      x[b][1] = x[b][3] = -7.5f * qsum[1];
       const unsigned char* kc = codes + b * 2 * kCodeBytes + lane * (4 * W);
       uint32_t ka[W], kb[W];
       load_words<W>(kc, ka);
@@ -274,53 +338,47 @@ struct Int4State {
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         const uint32_t u = ka[j], v = kb[j], u8 = u >> 8, v8 = v >> 8;
-        mma_16816(x[b], u & kLo, v & kLo, u & kHi, v & kHi, qb[2 * j][0], qb[2 * j][1]);
-        mma_16816(x[b], u8 & kLo, v8 & kLo, u8 & kHi, v8 & kHi, qb[2 * j + 1][0],
+        if (j == 0)
+          mma_16816_from(t[b], centre, u & kLo, v & kLo, u & kHi, v & kHi, qb[0][0], qb[0][1]);
+        else
+          mma_16816(t[b], u & kLo, v & kLo, u & kHi, v & kHi, qb[2 * j][0], qb[2 * j][1]);
+        mma_16816(t[b], u8 & kLo, v8 & kLo, u8 & kHi, v8 & kHi, qb[2 * j + 1][0],
                   qb[2 * j + 1][1]);
       }
     }
-    // ---- scores
-    float bmax[2] = {-INFINITY, -INFINITY};
-    float2 vp[2][2];
-    float smax = 0.f;
+    // ---- scores over row_scale: s (q . n - 7.5 sum q) + mid sum q
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 kp = param(par + b * 128, g + 8 * i);
         vp[b][i] = param(par + b * 128 + 64, g + 8 * i);
-        if (!in(b, i)) vp[b][i] = make_float2(0.f, 0.f);
-        smax = fmaxf(smax, vp[b][i].x);
+        if (kMask && g + 8 * i >= (b ? valid1 : valid0)) vp[b][i] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& y = x[b][2 * i + e];
-          y = fmaf(kp.x, y, kp.y * qsum[e]) * row_scale[e];
-          if (!in(b, i)) y = -INFINITY;
-          bmax[e] = fmaxf(bmax[e], y);
-        }
+        for (int e = 0; e < 2; ++e)
+          t[b][2 * i + e] = fmaf(kp.x, t[b][2 * i + e], kp.y * qsum[e]);
       }
-    const bool moved =
-        bmax[0] > m[0] + kLazyRescaleLog2 || bmax[1] > m[1] + kLazyRescaleLog2 || smax > vmax;
-    if (__any_sync(0xffffffffu, moved)) move(bmax, smax);
+    Weights r;
+    weigh<kMask>(t, vp, valid0, valid1, r);
+    if (__any_sync(0xffffffffu, r.out_of_range())) {
+      move<kMask>(t, vp, valid0, valid1);
+      weigh<kMask>(t, vp, valid0, valid1, r);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += r.p[e];
+      pmid[e] += r.pm[e];
+    }
     // ---- O^T += V^T P^T
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       uint32_t pb[2], lo[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float w[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float p = fast_exp2(x[b][2 * i + e] - ref[e]);
-          l[e] += p;
-          pmid[e] = fmaf(p, vp[b][i].y, pmid[e]);
-          w[e] = p * vp[b][i].x;  // at most 2^8 2^7: m is lazy by 2^8, and S >= the scale
-        }
-        const __half2 h = __floats2half2_rn(w[0], w[1]);
-        memcpy(&pb[i], &h, 4);
+        pb[i] = r.h[b][i];
         if constexpr (kResidual) {
-          const float2 r = __half22float2(h);
-          const __half2 rl = __floats2half2_rn(w[0] - r.x, w[1] - r.y);
+          const float2 f = half2_bits_to_float2(r.h[b][i]);
+          const __half2 rl = __floats2half2_rn(r.w[b][i][0] - f.x, r.w[b][i][1] - f.y);
           memcpy(&lo[i], &rl, 4);
           if constexpr (kRepeat) pb[i] = c < 2 ? pb[i] : lo[i];
           else lo[i] = transpose8(lo[i]);
