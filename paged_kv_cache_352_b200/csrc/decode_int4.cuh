@@ -307,7 +307,7 @@ struct Int4State {
       const bool first = m[e] == -INFINITY;  // nothing of this head has accumulated
       m[e] = fmaxf(m[e], bmax[e]);
       const float to = (m[e] == -INFINITY ? 0.f : m[e]) + shift;
-      const float alpha = first ? 1.f : exp2f(ref[e] - to);
+      const float alpha = first ? 1.f : fast_exp2(ref[e] - to);
       ref[e] = to;
       l[e] *= alpha;
       pmid[e] *= alpha;
@@ -406,17 +406,8 @@ struct Int4State {
     }
   }
 
-  // Sums the shares of the lanes: l and pmid over the tokens, the residual's
-  // columns into the heads'.
+  // Sums the lanes' shares of l and pmid.
   __device__ __forceinline__ void close() {
-    if constexpr (kRepeat) {  // columns 4-7 hold the residual's share of heads 0-3
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-#pragma unroll
-        for (int t = 0; t < MT; ++t) o[t][e] += __shfl_xor_sync(0xffffffffu, o[t][e], 2);
-        ow[e] += __shfl_xor_sync(0xffffffffu, ow[e], 2);
-      }
-    }
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -424,6 +415,10 @@ struct Int4State {
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], mask);
         pmid[e] += __shfl_xor_sync(0xffffffffu, pmid[e], mask);
       }
+    if constexpr (kRepeat) {  // columns 4-7 repeat the heads for the residual alone
+      pmid[0] = c < 2 ? pmid[0] : 0.f;
+      pmid[1] = c < 2 ? pmid[1] : 0.f;
+    }
   }
 
   // Unnormalised outputs (in units of 2^ref) of head 2c + e: dimensions
@@ -609,9 +604,9 @@ __global__ void __launch_bounds__(kInt4Warps * 32, kInt4CtasPerSm)
     const float mr = M[e] == -INFINITY ? 0.f : M[e];
     L[e] = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) L[e] = fmaf(exp2f(red_m[w][h] - mr), red_l[w][h], L[e]);
-    const float sc = exp2f(red_m[warp][h] - mr);
-    if (h < G) {
+    for (int w = 0; w < WARPS; ++w) L[e] = fmaf(fast_exp2(red_m[w][h] - mr), red_l[w][h], L[e]);
+    const float sc = fast_exp2(red_m[warp][h] - mr);
+    if (St::head(h) < G) {
 #pragma unroll
       for (int q = 0; q < W; ++q) {
         const float4 v = st.row4(e, q);
@@ -634,6 +629,13 @@ __global__ void __launch_bounds__(kInt4Warps * 32, kInt4CtasPerSm)
     for (int w = 1; w < WARPS; ++w) {
       const float4 u = red_acc[(w * POS + pos) * 32 + lane];
       v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    if constexpr (St::kRepeat) {  // the residual's share, from the lane of column h + 4
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float4 u = red_acc[(w * POS + pos) * 32 + (lane ^ 2)];
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      }
     }
     const int dim = 4 * W * st.g + 4 * q;
     const float Mh = e ? M[1] : M[0], Lh = e ? L[1] : L[0];
