@@ -412,12 +412,15 @@ int paged_decode_impl(void* out, const void* q, const void* k_cache, const void*
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
     return fail(PA_ERR_INVALID_ARG, "out, q and cache pointers must be 16-byte aligned");
   DecodeLayout lay;
-  // Over 4-bit caches a small batch keeps the shorter partitions of an unordered
-  // one: 4096-token partitions of 8 sequences of 32k-131k tokens leave a launch of
-  // 2.2 waves (142.9 us; 140.0 us with 2048-token ones).
+  // Over 4-bit caches a batch of up to 2 kSplitTargetUnits units keeps the 2048-token
+  // partitions of an unordered one: its launch is as long as its longest partition
+  // (128 sequences of 16-4096 tokens, 8 KV heads: 42.0 us with 4096-token partitions,
+  // 31.7 us with these, 35.3 us with 1024-token ones; 256 such sequences: 57.8, 62.3 and
+  // 74.3 us).
   const long long units = (long long)num_seqs * num_kv_heads;
   const bool small_int4 = cache_dtype == PA_INT4 && units < kSplitTargetUnits;
-  const bool ordered = seq_order != nullptr && !small_int4;
+  const bool ordered =
+      seq_order != nullptr && !(cache_dtype == PA_INT4 && units < 2 * kSplitTargetUnits);
   if (int st = decode_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
                              partition_tokens, ordered, &lay))
     return st;
