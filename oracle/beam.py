@@ -27,7 +27,8 @@ def all_scores(logits, beam_scores):
         top = x[k].max()
         if top == -math.inf or b == -math.inf:
             continue
-        out[k] = b + (x[k] - (top + math.log(np.exp(x[k] - top).sum())))
+        # x - top first: a row of values near the type's largest magnitude keeps its log V
+        out[k] = (x[k] - top) + (b - math.log(np.exp(x[k] - top).sum()))
     return out, bad
 
 

@@ -50,19 +50,6 @@ __device__ __forceinline__ float from_orderable(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-// Exponentials in base 2: e^x as 2^(x kLog2e - c), with c = fl(ref kLog2e) for a reference
-// ref close to the largest x, so that a term costs one FMA and one ex2. kLog2e is the float
-// below log2 e; what it lacks, kLog2eRest, matters where x is large and acts there like
-// a shift of the reference: sum e^x = 2^(c + ref kLog2eRest) sum 2^(x kLog2e - c) up to
-// |x - ref| kLog2eRest, 2^-25 of a term's exponent.
-constexpr float kLog2e = 1.44269502162933349609375f;
-constexpr double kLog2eRest = 1.9259629911266175e-8;  // log2 e - kLog2e
-constexpr double kLn2 = 0.69314718055994530942;
-
-__device__ __forceinline__ double base2_reference(float ref) {
-  return (double)__fmul_rn(ref, kLog2e) + (double)ref * kLog2eRest;
-}
-
 // (value, index) as one key: larger is better, ties to the smaller index. 0 is
 // below every candidate. -0 counts as 0.
 __device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
@@ -135,7 +122,10 @@ template <int kMergeThreads>
 __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& work, int tiles,
                                                int b, uint64_t* buffer) {
   constexpr int kWarps = kMergeThreads / 32;
-  __shared__ double offset[PA_BEAM_MAX];  // beam score less logsumexp, -inf for a dead beam
+  // a score is (x - largest) + offset: offset is the beam score less the logarithm of the
+  // sum of exponentials relative to the row's largest logit, -inf for a dead beam
+  __shared__ double offset[PA_BEAM_MAX];
+  __shared__ float largest[PA_BEAM_MAX];
   double* cs = reinterpret_cast<double*>(buffer);
   int64_t* cf = reinterpret_cast<int64_t*>(buffer + kMergeCap);
   const int beams = a.num_beams, vocab = a.vocab, select = a.select;
@@ -165,19 +155,20 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
     double S = 0.0;
     for (int t = lane; t < tiles; t += 32) {
       const float m = __ldcg(tile_max + row * tiles + t), s = __ldcg(tile_sum + row * tiles + t);
-      if (m > -INFINITY || s != s) S += (double)s * exp2(base2_reference(m) - base2_reference(M));
+      if (m > -INFINITY || s != s) S += (double)s * exp((double)m - (double)M);
     }
 #pragma unroll
     for (int mask = 16; mask > 0; mask >>= 1) S += __shfl_xor_sync(0xffffffffu, S, mask);
     if (lane == 0) {
       const float beam = a.beam_scores[row];
       double o = -INFINITY;
-      if (M > -INFINITY || S != S) o = (double)beam - kLn2 * (base2_reference(M) + log2(S));
+      if (M > -INFINITY || S != S) o = M < INFINITY ? (double)beam - log(S) : NAN;
       if (o != o || o == INFINITY) {  // a NaN or +inf among the logits, or as beam score
         report(a.dev_error, PA_DEVERR_LOGITS);
         o = -INFINITY;
       }
       offset[k] = o;
+      largest[k] = M;
     }
   }
   if (threadIdx.x == 0) count = 0;
@@ -187,7 +178,7 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
     s = -INFINITY;
     f = INT64_MAX;
     if (key != 0 && offset[k] > -INFINITY) {
-      s = offset[k] + (double)from_orderable((uint32_t)(key >> 32));
+      s = ((double)from_orderable((uint32_t)(key >> 32)) - (double)largest[k]) + offset[k];
       f = (int64_t)k * vocab + (uint32_t)~(uint32_t)key;
     }
   };
@@ -397,7 +388,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
   }
   // sum of exponentials relative to the warp's maximum; a NaN makes it NaN
   const float ref = wm == -INFINITY ? 0.f : wm;
-  const float minus_c = -__fmul_rn(ref, kLog2e);
+  constexpr float kLog2e = 1.4426950408889634f;
   float even = 0.f, odd = 0.f;  // summed in pairs by packed fp32 instructions
 #pragma unroll
   for (int i = 0; i < LOADS; ++i) {
@@ -405,9 +396,11 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
     Logits<T>::widen(u[i], f);
 #pragma unroll
     for (int e = 0; e < EPL; e += 2) {
-      float p = minus_c, q = minus_c;
-      ffma2(p, q, f[e], f[e + 1], kLog2e, kLog2e);
-      fadd2(even, odd, fast_exp2(p), fast_exp2(q));
+      // (x - ref) log2 e: the difference first, so that a row of the type's lowest or
+      // largest values is as exact as another
+      float p = f[e], q = f[e + 1];
+      fadd2(p, q, -ref, -ref);
+      fadd2(even, odd, fast_exp2(p * kLog2e), fast_exp2(q * kLog2e));
     }
   }
   float sum = even + odd;
@@ -453,7 +446,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
     for (int w = 0; w < kWarps; ++w)
       S += warp_sum[w] * (warp_max[w] == -INFINITY
                               ? 1.f
-                              : exp2f(__fmul_rn(warp_max[w], kLog2e) - __fmul_rn(M, kLog2e)));
+                              : expf(warp_max[w] - M));
     work.max[out] = M;
     work.sum[out] = S;
   }

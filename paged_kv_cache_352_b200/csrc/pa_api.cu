@@ -411,6 +411,10 @@ int paged_decode_impl(void* out, const void* q, const void* k_cache, const void*
     return fail(PA_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
     return fail(PA_ERR_INVALID_ARG, "out, q and cache pointers must be 16-byte aligned");
+  if (cache_dtype == PA_INT4 &&
+      (long long)num_blocks * num_kv_heads * (kBlockSize * row_bytes(head_dim, PA_INT4) / 64) >=
+          0xfffffffeLL)  // the kernel counts tile places in 64 bytes
+    return fail(PA_ERR_UNSUPPORTED, "4-bit caches of 2^38 bytes or more are not supported");
   DecodeLayout lay;
   // Over 4-bit caches a batch of up to 2 kSplitTargetUnits units keeps the 2048-token
   // partitions of an unordered one: its launch is as long as its longest partition

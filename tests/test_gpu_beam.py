@@ -146,6 +146,23 @@ def test_extreme_logits_and_scores():
     check(run(x, s, 12), x, s, 12)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_masks_of_the_lowest_value(dt):
+    """Tokens masked with the type's lowest value instead of -inf, a row of nothing else, one of
+    the largest, and a beam score that low."""
+    x, s = make(3, 3, 4500, dt, 15)
+    low, top = torch.finfo(TDT[dt]).min, torch.finfo(TDT[dt]).max
+    x[0:3][torch.rand(3, 4500, device="cuda") < 0.9] = low
+    x[3:6] = low                               # uniform: every token at -log V
+    x[6], x[7, :9] = top, top
+    s[0, 1] = torch.finfo(torch.float32).min
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run(x, s, 9, err=err)
+    assert err.item() == 0
+    check(out, x, s, 9)
+    assert abs(float(out[0][1, 0] - s[1].max()) + math.log(4500)) < 1e-5
+
+
 def test_padded_rows_stream_graph_and_two_calls_at_once():
     x, s = make(4, 4, 20000, "bf16", 21, pad=64)
     assert x.stride(0) == 20064

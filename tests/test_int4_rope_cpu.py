@@ -177,6 +177,7 @@ def test_int4_decode_refuses():
     assert st(_16=16) == L.PA_ERR_INVALID_ARG                      # split without a workspace
     assert st(_15=float("nan")) == L.PA_ERR_INVALID_ARG
     assert st(_0=None) == L.PA_ERR_INVALID_ARG and st(_2=ODD) == L.PA_ERR_INVALID_ARG
+    assert st(_14=1 << 29) == L.PA_ERR_UNSUPPORTED                 # places beyond 2^38 bytes
     assert st(_8=0) == L.PA_OK
 
 
