@@ -102,7 +102,8 @@ int pa_version(void);
  * PA_DEVERR_WAIT_TIMEOUT instead of spinning. This call lets a test drive that
  * path without a fault: the next decode kernel launch in the process (by any
  * pa_paged_decode* call; for pa_paged_decode_cascade* the launch that decodes
- * the shared and the own blocks) has each warp arm the barrier of its first block
+ * the shared and the own blocks; pa_paged_decode_int4 has no such waits and leaves
+ * the request to the next call that has) has each warp arm the barrier of its first block
  * without issuing the block's copy, and lowers the limit of the main loop's
  * waits to wait_limit_ns. That wait runs out, the warp reports
  * PA_DEVERR_WAIT_TIMEOUT, still waits (with the normal 1 s limit) for the
@@ -255,7 +256,11 @@ int pa_paged_decode_fp8(void* out, const void* q, const void* k_cache, const voi
  * and value.
  *
  * pa_paged_decode_int4: pa_paged_decode over these caches; q and out are of
- * type dtype (PA_F16 or PA_BF16). Workspace, plan and order as pa_paged_decode.
+ * type dtype (PA_F16 or PA_BF16). Workspace and order as pa_paged_decode. The
+ * library's choice of partitions (partition_tokens 0) is pa_paged_decode_plan's,
+ * but the unordered one also with a seq_order when num_seqs * num_kv_heads is
+ * below 2048; few sequences of many partitions merge in a second launch. A pool
+ * must be below 2^38 bytes (PA_ERR_UNSUPPORTED).
  *
  * pa_read_slots_int4: the inverse of the write, for callers that attend to
  * cached rows by other means (a prompt's later chunk, a comparison): row t of
@@ -448,7 +453,8 @@ int pa_paged_decode_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
                                    int head_dim, int max_context_len, int block_size,
                                    int partition_tokens, size_t* bytes);
 
-/* The split-KV plan pa_paged_decode (or pa_paged_decode_fp8) would use for these
+/* The split-KV plan pa_paged_decode (or pa_paged_decode_fp8; for
+ * pa_paged_decode_int4 see there) would use for these
  * arguments (ordered != 0: a seq_order is passed): blocks per partition, the
  * partitions per sequence the grid covers, and the kernel launches the call
  * makes (1; 2 when short partitions run one warp per partition followed by a

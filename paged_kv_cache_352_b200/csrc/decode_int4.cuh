@@ -21,9 +21,10 @@
 //     eight codes, w & 0x000f000f and w & 0x00f000f0 are operand registers, and
 //     the same masks of w >> 8 give the rest: 5 instructions for 8 codes. The
 //     powers of two are taken back in the query operand (1/16 at the dimensions
-//     of high nibbles) and in the fp32 results. Value codes, whose dimensions are
-//     rows of their own, take 4: the bytes w & 0x00ff00ff and their like, and the
-//     high nibbles, which a subtraction at the end takes out of the bytes' sums;
+//     of high nibbles) and in the fp32 results. (Value codes could do with 4, whole
+//     bytes and high nibbles whose sums are subtracted at the end; but the bytes' sums are
+//     16 times as large and a long context's mean is what is left of them: the error
+//     over 32k-131k tokens grew from 0.17% to 0.52%);
 //   - the cache layout (int4_cache.cuh) gives each lane the 16 bytes it feeds to
 //     its own registers, so lanes copy their own chunks by cp.async: no barrier,
 //     no lane that issues for the others, 9 copies per two blocks;
@@ -41,8 +42,8 @@
 // tokens g, g + 8 of heads 2c, 2c + 1; movmatrix turns the weights into the B
 // operand of
 // O^T = V^T P^T. A value word holds four dimensions of tokens 2p, 2p+1: word q of
-// pair c gives a0 (dimension 4Wg + 4q, as its byte) and a1 (+1), of pair c + 4 a2 and
-// a3; the upper bytes, dimensions +2 and +3 for the next m-tile. The result's columns are
+// pair c gives a0 (dimension 4Wg + 4q) and a1 (+1), of pair c + 4 a2 and a3;
+// shifted, dimensions +2 and +3 for the next m-tile. The result's columns are
 // heads 2c, 2c + 1 again. One more product with ones for V gives sum w.
 //
 // Precision. Products are exact, sums are fp32. q is brought below 2^15 by a
@@ -76,6 +77,7 @@ namespace {
 constexpr int kInt4Warps = 4;
 constexpr int kInt4Stages = 3;
 constexpr int kInt4CtasPerSm = 4;  // 128 registers a thread
+constexpr int kRecentre = 32;      // steps between recentrings of the output sums
 
 // A lane's four chunks of a block's codes: two of K, two of V.
 template <int CB>
@@ -157,7 +159,7 @@ struct Int4State {
   static constexpr int kTileBytes = int4_tile_bytes(D);
   static constexpr bool kResidual = std::is_same<T, __half>::value;
   static constexpr bool kRepeat = kResidual && G <= 4;  // columns 4-7 repeat heads 0-3
-  static constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u, kByte = 0x00ff00ffu;
+  static constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
 
   int g, c, lane;
   uint4 qraw[W];
@@ -397,19 +399,32 @@ struct Int4State {
         mma_16816(ow, kOnes, kOnes, kOnes, kOnes, lo[0], lo[1]);
 #pragma unroll
       for (int q = 0; q < W; ++q) {
-        // per word the bytes as they are, n_lo + 16 n_hi, and 16 n_hi: the low nibbles'
-        // sums follow by one subtraction at the end
-        const uint32_t a = va[q], d = vb[q];
-        const uint32_t a8 = __byte_perm(a, 0u, 0x4341), d8 = __byte_perm(d, 0u, 0x4341);
-        const uint32_t x0 = a & kByte, x1 = a & kHi, x2 = d & kByte, x3 = d & kHi;
-        const uint32_t y1 = a8 & kHi, y3 = d8 & kHi;
-        mma_16816(o[2 * q], x0, x1, x2, x3, pb[0], pb[1]);
-        mma_16816(o[2 * q + 1], a8, y1, d8, y3, pb[0], pb[1]);
+        const uint32_t a = va[q], d = vb[q], a8 = a >> 8, d8 = d >> 8;
+        mma_16816(o[2 * q], a & kLo, a & kHi, d & kLo, d & kHi, pb[0], pb[1]);
+        mma_16816(o[2 * q + 1], a8 & kLo, a8 & kHi, d8 & kLo, d8 & kHi, pb[0], pb[1]);
         if constexpr (kResidual && !kRepeat) {
-          mma_16816(o[2 * q], x0, x1, x2, x3, lo[0], lo[1]);
-          mma_16816(o[2 * q + 1], a8, y1, d8, y3, lo[0], lo[1]);
+          mma_16816(o[2 * q], a & kLo, a & kHi, d & kLo, d & kHi, lo[0], lo[1]);
+          mma_16816(o[2 * q + 1], a8 & kLo, a8 & kHi, d8 & kLo, d8 & kHi, lo[0], lo[1]);
         }
       }
+    }
+  }
+
+  // Takes 7.5 sum w out of the output sums so far. The matrix instruction's additions
+  // round towards zero, which costs half a step of the sum each: over codes of mean 7.5 the
+  // sums grow with the context while their centred part does not. Every kRecentre steps
+  // the sums start again from the centred part (an error of 2^-24 7.5 kRecentre of the
+  // weights' scale, whatever the length).
+  __device__ __forceinline__ void recentre() {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float w = -7.5f * ow[e];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        o[i][e] = fmaf(w, 5.9604644775390625e-8f, o[i][e]);           // 2^-24
+        o[i][2 + e] = fmaf(w, 9.5367431640625e-7f, o[i][2 + e]);      // 2^-20
+      }
+      ow[e] = 0.f;
     }
   }
 
@@ -432,9 +447,10 @@ struct Int4State {
   // 4W g + 4q .. + 3.
   __device__ __forceinline__ float4 row4(int e, int q) const {
     const float base = fmaf(-7.5f, ow[e], pmid[e]);
-    const float x = o[2 * q][2 + e], y = o[2 * q + 1][2 + e];  // 16 n of the high nibbles
-    return make_float4(fmaf(o[2 * q][e] - x, 16777216.f, base), fmaf(x, 1048576.f, base),
-                       fmaf(o[2 * q + 1][e] - y, 16777216.f, base), fmaf(y, 1048576.f, base));
+    return make_float4(fmaf(o[2 * q][e], 16777216.f, base),
+                       fmaf(o[2 * q][2 + e], 1048576.f, base),
+                       fmaf(o[2 * q + 1][e], 16777216.f, base),
+                       fmaf(o[2 * q + 1][2 + e], 1048576.f, base));
   }
 };
 
@@ -581,6 +597,7 @@ __global__ void __launch_bounds__(kInt4Warps * 32, kInt4CtasPerSm)
       st.template step<true>(codes, codes + Stage::kParOff, (miss & 1u) ? 0 : v0,
                              (miss & 2u) ? 0 : v0 - kBlockSize);
     stg = stg == STAGES - 1 ? 0 : stg + 1;
+    if ((j & (kRecentre - 1)) == kRecentre - 1) st.recentre();
   }
   cp_async_wait<0>();
 

@@ -278,6 +278,31 @@ def test_decode_warp_partitions(G):
     b.check(b.run(64), rows=[0, 3, 7, 31, 63])
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("part", [65536, 0])
+def test_decode_long_context_mean(dt, part):
+    """60000 tokens, in one partition and in the library's: the output is a mean of thousands of
+    values, a hundredth of one of them, and has to stay within the type's rounding of it. Bound
+    of the relative norm: half a step of the type (its root mean square is below) plus the
+    weights' share, 2^-11 rounded to bf16's operands (sqrt(1/3) of it in the mean, over the
+    centred codes), plus 64 additions of the matrix instruction at 2^-24 of 7.5 scale each."""
+    b = Batch([60000], 4, 1, 128, dt, 43)
+    out = b.run(part)
+    kc, vc = b.kc.cpu().numpy(), b.vc.cpu().numpy()
+    blocks = b.tables[0]
+    k = np.concatenate([x for x in I4.dequantize_cache(kc, False)[blocks, 0]])[:60000]
+    v = np.concatenate([x for x in I4.dequantize_cache(vc, True)[blocks, 0]])[:60000]
+    scale = float(params(vc)[blocks, 0].reshape(-1, 2)[:60000, 0].max())
+    got = out_to_f64(out[0], dt)
+    for h in range(4):
+        ref = I4.softmax_attention(bits_to_f64(b.q, dt)[0, h], k, v, b.scale)
+        rms = float(np.sqrt((ref ** 2).mean()))
+        step = torch.finfo(TDT[dt]).eps / 2
+        bound = step + (2.0 ** -11 if dt == "bf16" else 2.0 ** -20) + 64 * 2.0 ** -24 * 7.5 * scale / rms
+        assert np.linalg.norm(got[h] - ref) <= bound * np.linalg.norm(ref), (
+            h, np.linalg.norm(got[h] - ref) / np.linalg.norm(ref), bound)
+
+
 def test_decode_value_scales_of_every_size():
     """Value rows whose scales differ by 2^20, rising, falling and zero: the reference of the
     weights moves, and small rows keep their share when the large ones carry no weight."""
