@@ -272,56 +272,64 @@ def _int4_dims(k_cache, v_cache):
     return nb, hkv, bs, d
 
 
-class _On:
-    """The device of a call's tensors: ``ptr`` gives a tensor's address after checking that it
-    lies there, and ``call`` runs a library call with that device current, on the given
-    stream or the device's current one."""
+# The calls below take many tensors and are made once per layer and token, so their
+# marshalling is kept short: device indices and dtype objects are compared, not formatted.
 
-    def __init__(self, t):
-        self.dev = t.device
-        if self.dev.type != "cuda":
-            raise PAError(PA_ERR_INVALID_ARG, f"tensors must be on a CUDA device, got {self.dev}")
+def _index(t, name) -> int:
+    """Index of the CUDA device that holds ``t``; every tensor of a call has to be on it."""
+    idx = t.get_device()
+    if idx < 0:
+        raise PAError(PA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
+    return idx
 
-    def ptr(self, t, name, dtype=None, contiguous=True):
-        if t is None:
-            return None
-        if t.device != self.dev:
-            raise PAError(PA_ERR_INVALID_ARG, f"{name} is on {t.device}, expected {self.dev}")
-        if dtype is not None and t.dtype is not dtype:
-            raise PAError(PA_ERR_INVALID_ARG, f"{name} must be {dtype}, got {t.dtype}")
-        if contiguous and not t.is_contiguous():
-            raise PAError(PA_ERR_INVALID_ARG, f"{name} must be contiguous")
-        return t.data_ptr()
 
-    def rows(self, t, name, heads, d, dtype=None):
-        """Address and token stride of a [T, heads, d] tensor whose rows are dense per token (the
-        stride of a dense one when T is 1, where a tensor's own may be anything)."""
-        T = t.shape[0]
-        stride = t.stride()
-        if T and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
-            raise PAError(PA_ERR_INVALID_ARG, f"{name} rows must be dense per token")
-        return self.ptr(t, name, dtype, False), (stride[0] if T > 1 else heads * d)
+def _refuse(t, idx, name, dtype):
+    if t.get_device() != idx:
+        raise PAError(PA_ERR_INVALID_ARG, f"{name} is on {t.device}, expected cuda:{idx}")
+    if t.dtype is not dtype:
+        raise PAError(PA_ERR_INVALID_ARG, f"{name} must be {dtype}, got {t.dtype}")
+    raise PAError(PA_ERR_INVALID_ARG, f"{name} must be contiguous")
 
-    def call(self, fn, *args, stream=None):
-        torch = _torch()
-        idx = self.dev.index
-        if torch.cuda.current_device() == idx:
-            return _check(fn(*args, _raw_stream(stream, idx)))
+
+def _addr(t, idx, name, dtype):
+    """Address of a contiguous tensor of type ``dtype`` on device ``idx``."""
+    if t.get_device() != idx or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, idx, name, dtype)
+    return t.data_ptr()
+
+
+def _opt(t, idx, name, dtype):
+    return None if t is None else _addr(t, idx, name, dtype)
+
+
+def _rows(t, idx, name, dtype):
+    """Address and token stride of a [T, heads, d] tensor whose rows are dense per token (the
+    stride of a dense one when T is 1, where a tensor's own may be anything)."""
+    if t.get_device() != idx or t.dtype is not dtype:
+        _refuse(t, idx, name, dtype)
+    T, heads, d = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), heads * d
+    st, sh, s1 = t.stride()
+    if s1 != 1 or (heads > 1 and sh != d):
+        raise PAError(PA_ERR_INVALID_ARG, f"{name} rows must be dense per token")
+    return t.data_ptr(), st if T > 1 else heads * d
+
+
+def _launch(idx, fn, args, stream):
+    """fn(*args, stream) with device ``idx`` current, on the given stream or its current one."""
+    torch = _torch()
+    if torch.cuda.current_device() == idx:
+        _check(fn(*args, _raw_stream(stream, idx)))
+    else:
         with torch.cuda.device(idx):
-            return _check(fn(*args, _raw_stream(stream, idx)))
+            _check(fn(*args, _raw_stream(stream, idx)))
 
 
 def _raw_stream(stream, index):
     if stream is None:
         return _torch()._C._cuda_getCurrentRawStream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _check_rows(key, value, hkv, d):
-    T = key.shape[0]
-    if key.shape[1:] != (hkv, d) or value.shape != key.shape:
-        raise PAError(PA_ERR_INVALID_ARG, "key/value must be [T, num_kv_heads, head_dim]")
-    return T
 
 
 # --------------------------------------------------------------------------
@@ -540,15 +548,19 @@ def pa_paged_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, ma
 def _int4_rows(fn, key, value, k_cache, v_cache, slot_mapping, dev_error, stream):
     torch = _torch()
     nb, hkv, bs, d = _int4_dims(k_cache, v_cache)
-    T = _check_rows(key, value, hkv, d)
+    shape = key.shape
+    if len(shape) != 3 or shape[1] != hkv or shape[2] != d or value.shape != shape:
+        raise PAError(PA_ERR_INVALID_ARG, "key/value must be [T, num_kv_heads, head_dim]")
+    T = shape[0]
     if slot_mapping.shape != (T,):
         raise PAError(PA_ERR_INVALID_ARG, "slot_mapping must be [T]")
-    on = _On(k_cache)
-    kp, ks = on.rows(key, "key", hkv, d)
-    vp, vs = on.rows(value, "value", hkv, d, key.dtype)
-    on.call(fn, kp, vp, ks, vs, on.ptr(k_cache, "k_cache"), on.ptr(v_cache, "v_cache"),
-            on.ptr(slot_mapping, "slot_mapping", torch.int64), T, hkv, d, bs, nb, dtype_code(key),
-            on.ptr(dev_error, "dev_error", torch.int32), stream=stream)
+    idx, u8 = _index(k_cache, "k_cache"), torch.uint8
+    kp, ks = _rows(key, idx, "key", key.dtype)
+    vp, vs = _rows(value, idx, "value", key.dtype)
+    _launch(idx, fn, (kp, vp, ks, vs, _addr(k_cache, idx, "k_cache", u8),
+                      _addr(v_cache, idx, "v_cache", u8),
+                      _addr(slot_mapping, idx, "slot_mapping", torch.int64), T, hkv, d, bs, nb,
+                      dtype_code(key), _opt(dev_error, idx, "dev_error", torch.int32)), stream)
 
 
 def pa_reshape_and_cache_int4(key, value, k_cache, v_cache, slot_mapping, dev_error=None,
@@ -582,15 +594,17 @@ def pa_paged_decode_int4(out, q, k_cache, v_cache, block_tables, context_lens, m
         raise PAError(PA_ERR_INVALID_ARG, "block_tables must be [B, max_blocks], context_lens [B]")
     if seq_order is not None and seq_order.shape != (B,):
         raise PAError(PA_ERR_INVALID_ARG, "seq_order must be [num_seqs]")
-    on = _On(q)
-    i32 = torch.int32
-    on.call(lib().pa_paged_decode_int4, on.ptr(out, "out", q.dtype), on.ptr(q, "q"),
-            on.ptr(k_cache, "k_cache"), on.ptr(v_cache, "v_cache"),
-            on.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
-            on.ptr(context_lens, "context_lens", i32), on.ptr(seq_order, "seq_order", i32), B,
-            int(max_context_len), hq, hkv, d, bs, nb, scale, int(partition_tokens),
-            on.ptr(workspace, "workspace"), 0 if workspace is None else workspace.nbytes,
-            on.ptr(dev_error, "dev_error", i32), dtype_code(q), stream=stream)
+    idx, i32, u8 = _index(q, "q"), torch.int32, torch.uint8
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = _addr(workspace, idx, "workspace", workspace.dtype), workspace.nbytes
+    _launch(idx, lib().pa_paged_decode_int4, (
+        _addr(out, idx, "out", q.dtype), _addr(q, idx, "q", q.dtype),
+        _addr(k_cache, idx, "k_cache", u8), _addr(v_cache, idx, "v_cache", u8),
+        _addr(block_tables, idx, "block_tables", i32), block_tables.shape[1],
+        _addr(context_lens, idx, "context_lens", i32), _opt(seq_order, idx, "seq_order", i32), B,
+        int(max_context_len), hq, hkv, d, bs, nb, scale, int(partition_tokens), ws, ws_bytes,
+        _opt(dev_error, idx, "dev_error", i32), dtype_code(q)), stream)
 
 
 def pa_rope_table(num_positions, rotary_dim, theta=10000.0) -> np.ndarray:
@@ -606,27 +620,32 @@ def _rope(fn, dims, cache_ok, q_out, q, key, value, positions, cos_sin, k_cache,
           slot_mapping, interleaved, scales, dev_error, stream):
     torch = _torch()
     nb, hkv, bs, d = dims
-    T = _check_rows(key, value, hkv, d)
+    shape, q_shape, per_token = key.shape, q.shape, positions.shape
+    if len(shape) != 3 or shape[1] != hkv or shape[2] != d or value.shape != shape:
+        raise PAError(PA_ERR_INVALID_ARG, "key/value must be [T, num_kv_heads, head_dim]")
+    T = shape[0]
     if not cache_ok:
         raise PAError(PA_ERR_INVALID_ARG, "k_cache/v_cache are not of the call's element type")
-    if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or q_out.shape != q.shape:
+    if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d or q_out.shape != q_shape:
         raise PAError(PA_ERR_INVALID_ARG, "q/q_out must be [T, num_q_heads, head_dim] in key's "
                                           "dtype")
-    if positions.shape != (T,) or slot_mapping.shape != (T,) or cos_sin.dim() != 2:
+    if len(per_token) != 1 or per_token[0] != T or slot_mapping.shape != per_token or \
+            cos_sin.dim() != 2:
         raise PAError(PA_ERR_INVALID_ARG, "positions and slot_mapping must be [T], cos_sin "
                                           "[num_positions, rotary_dim]")
-    on = _On(k_cache)
-    hq, dt = q.shape[1], key.dtype
-    qop, qos = on.rows(q_out, "q_out", hq, d, dt)
-    qp, qs = on.rows(q, "q", hq, d, dt)
-    kp, ks = on.rows(key, "key", hkv, d)
-    vp, vs = on.rows(value, "value", hkv, d, dt)
+    idx, dt, i64 = _index(k_cache, "k_cache"), key.dtype, torch.int64
+    qop, qos = _rows(q_out, idx, "q_out", dt)
+    qp, qs = _rows(q, idx, "q", dt)
+    kp, ks = _rows(key, idx, "key", dt)
+    vp, vs = _rows(value, idx, "value", dt)
     P, R = cos_sin.shape
-    on.call(fn, qop, qp, kp, vp, qos, qs, ks, vs, on.ptr(positions, "positions", torch.int64),
-            on.ptr(cos_sin, "cos_sin", torch.float32), P, R, int(bool(interleaved)),
-            on.ptr(k_cache, "k_cache"), on.ptr(v_cache, "v_cache"),
-            on.ptr(slot_mapping, "slot_mapping", torch.int64), T, hq, hkv, d, bs, nb,
-            dtype_code(key), *scales, on.ptr(dev_error, "dev_error", torch.int32), stream=stream)
+    ct = k_cache.dtype
+    _launch(idx, fn, (
+        qop, qp, kp, vp, qos, qs, ks, vs, _addr(positions, idx, "positions", i64),
+        _addr(cos_sin, idx, "cos_sin", torch.float32), P, R, 1 if interleaved else 0,
+        _addr(k_cache, idx, "k_cache", ct), _addr(v_cache, idx, "v_cache", ct),
+        _addr(slot_mapping, idx, "slot_mapping", i64), T, q_shape[1], hkv, d, bs, nb,
+        dtype_code(key), *scales, _opt(dev_error, idx, "dev_error", torch.int32)), stream)
 
 
 def pa_rope_and_cache(q_out, q, key, value, positions, cos_sin, k_cache, v_cache, slot_mapping,
@@ -703,13 +722,15 @@ def pa_beam_select(scores, parents, tokens, logits, beam_scores, workspace, dev_
     per16 = 4 if logits.dtype == torch.float32 else 8
     # one row's stride is not used: any that holds it will do
     stride = logits.stride(0) if rows > 1 else -(-V // per16) * per16
-    on = _On(logits)
-    f32, i32 = torch.float32, torch.int32
-    on.call(lib().pa_beam_select, on.ptr(scores, "scores", f32), on.ptr(parents, "parents", i32),
-            on.ptr(tokens, "tokens", i32), on.ptr(logits, "logits", None, False), stride,
-            on.ptr(beam_scores, "beam_scores", f32), B, K, V, n, on.ptr(workspace, "workspace"),
-            0 if workspace is None else workspace.nbytes, on.ptr(dev_error, "dev_error", i32),
-            _logits_code(logits.dtype), stream=stream)
+    idx, f32, i32 = _index(logits, "logits"), torch.float32, torch.int32
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = _addr(workspace, idx, "workspace", workspace.dtype), workspace.nbytes
+    _launch(idx, lib().pa_beam_select, (
+        _addr(scores, idx, "scores", f32), _addr(parents, idx, "parents", i32),
+        _addr(tokens, idx, "tokens", i32), logits.data_ptr(), stride,
+        _addr(beam_scores, idx, "beam_scores", f32), B, K, V, n, ws, ws_bytes,
+        _opt(dev_error, idx, "dev_error", i32), _logits_code(logits.dtype)), stream)
 
 
 def pa_paged_decode_cascade_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
