@@ -349,8 +349,15 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
     return Logits<T>::narrow(f);
   };
   uint4 u[LOADS];
+  if (base + kBeamThreads * kPer <= vocab) {  // the whole tile: one address, no tests
+    const uint4* from = reinterpret_cast<const uint4*>(x + base) + threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) u[i] = load(base + (i * kBeamThreads + (int)threadIdx.x) * EPL);
+    for (int i = 0; i < LOADS; ++i) u[i] = __ldg(from + i * kBeamThreads);
+  } else {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i)
+      u[i] = load(base + (i * kBeamThreads + (int)threadIdx.x) * EPL);
+  }
   if (threadIdx.x == 0) {
     count = 0;
     threshold = 0;
@@ -400,7 +407,8 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
       // largest values is as exact as another
       float p = f[e], q = f[e + 1];
       fadd2(p, q, -ref, -ref);
-      fadd2(even, odd, fast_exp2(p * kLog2e), fast_exp2(q * kLog2e));
+      fmul2(p, q, kLog2e);
+      fadd2(even, odd, fast_exp2(p), fast_exp2(q));
     }
   }
   float sum = even + odd;

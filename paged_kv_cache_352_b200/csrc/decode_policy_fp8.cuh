@@ -474,15 +474,6 @@ struct Fp8TensorPairPolicy : Fp8TensorPolicy<T, D, G> {
 // CUDA cores over an E4M3 cache
 // ---------------------------------------------------------------------------
 
-// (d0, d1) *= (a, a) with sm_100's packed fp32 multiply.
-__device__ __forceinline__ void fmul2(float& d0, float& d1, float a) {
-  asm("{\n\t.reg .b64 ra, rd;\n\t"
-      "mov.b64 ra, {%2, %2};\n\tmov.b64 rd, {%0, %1};\n\t"
-      "mul.f32x2 rd, rd, ra;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "+f"(d0), "+f"(d1)
-      : "f"(a));
-}
-
 // d + a.lo * b.lo + a.hi * b.hi for two packed halves each: sm_100's
 // mixed-precision FMA takes half operands and an fp32 addend; a product of two
 // halves is exact in fp32, so each step rounds once, as an fp32 fmaf would.

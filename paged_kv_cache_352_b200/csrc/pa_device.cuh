@@ -237,6 +237,15 @@ __device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, 
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
+// (d0, d1) *= (a, a) with sm_100's packed fp32 multiply.
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a) {
+  asm("{\n\t.reg .b64 ra, rd;\n\t"
+      "mov.b64 ra, {%2, %2};\n\tmov.b64 rd, {%0, %1};\n\t"
+      "mul.f32x2 rd, rd, ra;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a));
+}
+
 // (d0, d1) += (a0, a1), packed as above.
 __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1) {
   asm("{\n\t.reg .b64 ra, rd;\n\t"
