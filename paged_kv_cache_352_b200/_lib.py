@@ -380,8 +380,8 @@ def pa_swap_blocks(src_k, src_v, dst_k, dst_v, pairs, stream=None):
     """Copy blocks ``pairs[i, 0]`` of the source pool over ``pairs[i, 1]`` of the
     destination pool; pools are CUDA tensors or pinned host tensors."""
     s_nb, hkv, bs, d, code = _pool_dims(src_k, src_v)
-    d_nb, hkv2, bs2, d2, _ = _pool_dims(dst_k, dst_v)
-    if (hkv, bs, d) != (hkv2, bs2, d2) or src_k.dtype != dst_k.dtype:
+    d_nb, hkv2, bs2, d2, code2 = _pool_dims(dst_k, dst_v)
+    if (hkv, bs, d, code) != (hkv2, bs2, d2, code2) or src_k.dtype != dst_k.dtype:
         raise PAError(PA_ERR_INVALID_ARG, "source and destination pools differ in layout")
     p = np.ascontiguousarray(np.asarray(pairs, dtype=np.int64).reshape(-1, 2))
     with _device(src_k, dst_k):
@@ -1219,6 +1219,7 @@ class Scheduler:
         self.io_dtype = code
         self.fp8 = fp8_scales is not None
         self.int4 = int4
+        self._int4_pool = (num_kv_heads, self.block_size, head_dim)
 
     def set_cascade(self, mode: int) -> None:
         """When the executor decodes sequences that share leading blocks through
@@ -1242,6 +1243,13 @@ class Scheduler:
         if (code == PA_FP8_E4M3) != getattr(self, "fp8", False) or (
                 code == PA_INT4) != getattr(self, "int4", False):
             raise PAError(PA_ERR_INVALID_ARG, "cache element type differs from the attached one")
+        if code == PA_INT4:
+            want = [(k_cache, v_cache, self.num_blocks)]
+            if host_k is not None and host_v is not None:
+                want.append((host_k, host_v, self.num_host_blocks))
+            dims = [(_int4_dims(k, v), n) for k, v, n in want]
+            if any(d[0] < n or d[1:] != self._int4_pool for d, n in dims):
+                raise PAError(PA_ERR_INVALID_ARG, "4-bit pools differ from the attached sizes")
         cdt = k_cache.dtype
         dt = q.dtype
         host = lambda t, n: None if t is None else _pool_ptr(t, n)

@@ -197,3 +197,26 @@ def test_binding_refuses_cpu_tensors_and_other_pools():
         assert e.value.code in (L.PA_ERR_INVALID_ARG, L.PA_ERR_UNSUPPORTED)
     with pytest.raises(pa.PAError):
         pa.pa_read_slots_int4(x[:, :1], x, pool, pool, slots)
+
+
+@pytest.mark.parametrize("last", [64, 128])
+def test_swap_refuses_pools_of_other_formats(last):
+    """An 8-bit and a 4-bit pool of one head_dim are both bytes, with blocks of other sizes."""
+    codes = torch.zeros(3, 2, 16, last, dtype=torch.uint8)
+    int4 = torch.zeros(3, 2, 16, last // 2 + 4, dtype=torch.uint8)
+    for src, dst in ((codes, int4), (int4, codes)):
+        with pytest.raises(pa.PAError, match="differ in layout"):
+            pa.pa_swap_blocks(src, src, dst, dst, [(0, 1)])
+
+
+def test_scheduler_refuses_4_bit_pools_of_other_sizes():
+    s = pa.Scheduler(4, 16, num_host_blocks=2)
+    # what attach() leaves: it allocates on the device, which this test does without
+    s.int4, s.fp8, s._int4_pool = True, False, (2, 16, 64)
+    pool = lambda n, h, d: torch.zeros(n, h, 16, d // 2 + 4, dtype=torch.uint8)
+    x = torch.zeros(1, 2, 64, dtype=torch.float16)
+    run = lambda k, hk: s.execute(k, k, hk, hk, None, None, x, x, x, x, 1.0)
+    for k, hk in ((pool(3, 2, 64), None), (pool(4, 1, 64), None), (pool(4, 2, 128), None),
+                  (pool(4, 2, 64), pool(1, 2, 64)), (pool(4, 2, 64), pool(2, 2, 128))):
+        with pytest.raises(pa.PAError, match="attached sizes"):
+            run(k, hk)
