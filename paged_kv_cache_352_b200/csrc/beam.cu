@@ -38,8 +38,9 @@ namespace {
 
 constexpr int kBeamThreads = 256;
 constexpr int kGroups = 64;       // groups of a tile whose maxima bound the N-th largest
-constexpr int kTileCap = 2048;    // candidates a tile ranks at once
+constexpr int kPieceCap = 2048;    // candidates a piece ranks at once
 constexpr int kMergeCap = 1024;   // candidates a sequence ranks at once
+constexpr int kMaxPer = 16;       // chunks of a CTA's share
 
 // Floats in the order of unsigned integers (NaN aside).
 __device__ __forceinline__ uint32_t orderable(float x) {
@@ -66,13 +67,19 @@ struct Logits {
   }
   static __device__ __forceinline__ float one(const T* p) { return static_cast<float>(*p); }
   // the largest (NaN ignored), two at a time
-  static __device__ __forceinline__ float largest(const uint4& u) {
+  template <int N>
+  static __device__ __forceinline__ float largest(const uint4 (&u)[N]) {
     using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2,
                                          __nv_bfloat162>::type;
-    T2 h[4];
-    memcpy(h, &u, sizeof(u));
-    const T2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-    return fmaxf(static_cast<float>(m.x), static_cast<float>(m.y));
+    T2 m[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      T2 h[4];
+      memcpy(h, &u[i], sizeof(u[i]));
+      m[i] = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+      if (i) m[0] = __hmax2(m[0], m[i]);
+    }
+    return fmaxf(static_cast<float>(m[0].x), static_cast<float>(m[0].y));
   }
   static __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
     T r[8];
@@ -90,10 +97,16 @@ struct Logits<float> {
     memcpy(f, &u, sizeof(u));
   }
   static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
-  static __device__ __forceinline__ float largest(const uint4& u) {
-    float f[4];
-    widen(u, f);
-    return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
+  template <int N>
+  static __device__ __forceinline__ float largest(const uint4 (&u)[N]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float f[4];
+      widen(u[i], f);
+      m = fmaxf(m, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+    }
+    return m;
   }
   static __device__ __forceinline__ uint4 narrow(const float (&f)[4]) {
     uint4 u;
@@ -101,6 +114,18 @@ struct Logits<float> {
     return u;
   }
 };
+
+// The 16 bytes of logits at `at`, -inf past the row. Called for a row's last chunk and
+// for candidates only: out of the way of the loop over whole chunks.
+template <typename T>
+__device__ __noinline__ uint4 load_bounded(const T* x, int at, int vocab) {
+  constexpr int EPL = Logits<T>::kPerLoad;
+  if (at + EPL <= vocab) return __ldg(reinterpret_cast<const uint4*>(x + at));
+  float f[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) f[e] = at + e < vocab ? Logits<T>::one(x + at + e) : -INFINITY;
+  return Logits<T>::narrow(f);
+}
 
 // The workspace's parts.
 struct Work {
@@ -115,28 +140,34 @@ __device__ __forceinline__ bool before(double s, int64_t f, double t, int64_t g)
   return s > t || (s == t && f < g);
 }
 
-// Sequence b by one CTA: its rows' logsumexp, then its best candidates. `buffer`: shared
-// memory of kMergeCap (double, int64) pairs. The tiles' results were written by other
-// CTAs: they are read past L1.
-template <int kMergeThreads>
-__device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& work, int tiles,
-                                               int b, uint64_t* buffer) {
-  constexpr int kWarps = kMergeThreads / 32;
+// Shared memory of a sequence's merge.
+template <int kWarps>
+struct MergeShared {
   // a score is (x - largest) + offset: offset is the beam score less the logarithm of the
   // sum of exponentials relative to the row's largest logit, -inf for a dead beam
-  __shared__ double offset[PA_BEAM_MAX];
-  __shared__ float largest[PA_BEAM_MAX];
-  double* cs = reinterpret_cast<double*>(buffer);
-  int64_t* cf = reinterpret_cast<int64_t*>(buffer + kMergeCap);
+  __align__(16) double offset[PA_BEAM_MAX];
+  __align__(16) float largest[PA_BEAM_MAX];
+  __align__(16) double group_max[kGroups];
+  __align__(16) double warp_best[kWarps];
+  __align__(16) double best_score[kWarps];
+  __align__(16) int64_t best_index[kWarps];
+  __align__(16) int count;
+};
+
+// Sequence b by one CTA: its rows' logsumexp, then its best candidates. cs, cf: shared
+// memory for kMergeCap candidates. The pieces' results were written by other CTAs: they
+// are read past L1.
+template <int kMergeThreads>
+__device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& work, int pieces,
+                                               int b, MergeShared<kMergeThreads / 32>& sh,
+                                               double* cs, int64_t* cf) {
+  constexpr int kWarps = kMergeThreads / 32;
   const int beams = a.num_beams, vocab = a.vocab, select = a.select;
-  const float* tile_max = work.max;
-  const float* tile_sum = work.sum;
-  const uint64_t* tile_keys = work.keys;
-  __shared__ double group_max[kGroups];
-  __shared__ double warp_best[kWarps];
-  __shared__ int count;
+  const float* piece_max = work.max;
+  const float* piece_sum = work.sum;
+  const uint64_t* piece_keys = work.keys;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_beam = tiles * select;
+  const int per_beam = pieces * select;
   const int total = beams * per_beam;
   // this thread's first candidates, on their way while the rows' sums are added up
   constexpr int kAhead = 4;
@@ -144,17 +175,17 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
 #pragma unroll
   for (int j = 0; j < kAhead; ++j) {
     const int i = threadIdx.x + j * kMergeThreads;
-    ahead[j] = i < total ? __ldcg(tile_keys + (size_t)b * total + i) : 0;
+    ahead[j] = i < total ? __ldcg(piece_keys + (size_t)b * total + i) : 0;
   }
   for (int k = warp; k < beams; k += kWarps) {
     const size_t row = (size_t)b * beams + k;
     float M = -INFINITY;
-    for (int t = lane; t < tiles; t += 32) M = fmaxf(M, __ldcg(tile_max + row * tiles + t));
+    for (int t = lane; t < pieces; t += 32) M = fmaxf(M, __ldcg(piece_max + row * pieces + t));
 #pragma unroll
     for (int mask = 16; mask > 0; mask >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, mask));
     double S = 0.0;
-    for (int t = lane; t < tiles; t += 32) {
-      const float m = __ldcg(tile_max + row * tiles + t), s = __ldcg(tile_sum + row * tiles + t);
+    for (int t = lane; t < pieces; t += 32) {
+      const float m = __ldcg(piece_max + row * pieces + t), s = __ldcg(piece_sum + row * pieces + t);
       if (m > -INFINITY || s != s) S += (double)s * exp((double)m - (double)M);
     }
 #pragma unroll
@@ -167,25 +198,25 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
         report(a.dev_error, PA_DEVERR_LOGITS);
         o = -INFINITY;
       }
-      offset[k] = o;
-      largest[k] = M;
+      sh.offset[k] = o;
+      sh.largest[k] = M;
     }
   }
-  if (threadIdx.x == 0) count = 0;
+  if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
   auto score_key = [&](int i, uint64_t key, double& s, int64_t& f) {
     const int k = i / per_beam;
     s = -INFINITY;
     f = INT64_MAX;
-    if (key != 0 && offset[k] > -INFINITY) {
-      s = ((double)from_orderable((uint32_t)(key >> 32)) - (double)largest[k]) + offset[k];
+    if (key != 0 && sh.offset[k] > -INFINITY) {
+      s = ((double)from_orderable((uint32_t)(key >> 32)) - (double)sh.largest[k]) + sh.offset[k];
       f = (int64_t)k * vocab + (uint32_t)~(uint32_t)key;
     }
   };
   auto score_of = [&](int i, double& s, int64_t& f) {
-    score_key(i, __ldcg(tile_keys + (size_t)b * total + i), s, f);
+    score_key(i, __ldcg(piece_keys + (size_t)b * total + i), s, f);
   };
-  // as in a tile: the select-th largest of 64 groups' maxima bounds the result from below
+  // as in a piece: the select-th largest of 64 groups' maxima bounds the result from below
   double top = -INFINITY;
   double as[kAhead];
   int64_t af[kAhead];
@@ -206,15 +237,15 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
 #pragma unroll
   for (int mask = 1; mask < kGroupLanes; mask <<= 1)
     top = fmax(top, __shfl_xor_sync(0xffffffffu, top, mask));  // (never NaN)
-  if (threadIdx.x % kGroupLanes == 0) group_max[threadIdx.x / kGroupLanes] = top;
+  if (threadIdx.x % kGroupLanes == 0) sh.group_max[threadIdx.x / kGroupLanes] = top;
   __syncthreads();
   {
     // kGroupLanes threads count for each group
-    const double p = group_max[threadIdx.x / kGroupLanes];
+    const double p = sh.group_max[threadIdx.x / kGroupLanes];
     int rank = 0;
 #pragma unroll
     for (int i = 0; i < kGroups / kGroupLanes; ++i)
-      rank += group_max[i * kGroupLanes + threadIdx.x % kGroupLanes] >= p;
+      rank += sh.group_max[i * kGroupLanes + threadIdx.x % kGroupLanes] >= p;
 #pragma unroll
     for (int mask = 1; mask < kGroupLanes; mask <<= 1)
       rank += __shfl_xor_sync(0xffffffffu, rank, mask);
@@ -224,15 +255,15 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
       const double o = __shfl_xor_sync(0xffffffffu, best, mask);
       best = o > best ? o : best;
     }
-    if (lane == 0) warp_best[warp] = best;
+    if (lane == 0) sh.warp_best[warp] = best;
   }
   __syncthreads();
-  double lowest = warp_best[0];
+  double lowest = sh.warp_best[0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) lowest = warp_best[w] > lowest ? warp_best[w] : lowest;
+  for (int w = 1; w < kWarps; ++w) lowest = sh.warp_best[w] > lowest ? sh.warp_best[w] : lowest;
   auto collect = [&](double s, int64_t f) {
     if (s > -INFINITY && s >= lowest) {
-      const int at = atomicAdd(&count, 1);
+      const int at = atomicAdd(&sh.count, 1);
       if (at < kMergeCap) {
         cs[at] = s;
         cf[at] = f;
@@ -248,7 +279,7 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
     collect(s, f);
   }
   __syncthreads();
-  const int n = count;
+  const int n = sh.count;
   const size_t out = (size_t)b * select;
   auto put = [&](int rank, double s, int64_t f) {
     a.scores[out + rank] = (float)s;
@@ -267,8 +298,6 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
     return;
   }
   // more equal candidates than the buffer holds: one at a time
-  __shared__ double bs[kWarps];
-  __shared__ int64_t bf[kWarps];
   double ls = INFINITY;
   int64_t lf = -1;
   for (int r = 0; r < select; ++r) {
@@ -294,14 +323,14 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
     }
     __syncthreads();
     if (lane == 0) {
-      bs[warp] = s;
-      bf[warp] = f;
+      sh.best_score[warp] = s;
+      sh.best_index[warp] = f;
     }
     __syncthreads();
     for (int w = 0; w < kWarps; ++w)
-      if (before(bs[w], bf[w], s, f)) {
-        s = bs[w];
-        f = bf[w];
+      if (before(sh.best_score[w], sh.best_index[w], s, f)) {
+        s = sh.best_score[w];
+        f = sh.best_index[w];
       }
     if (threadIdx.x == 0) put(r, s, f);
     ls = s;
@@ -312,222 +341,301 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
 constexpr int kMergeThreads = 512;
 
 __global__ void __launch_bounds__(kMergeThreads)
-    beam_merge_kernel(const BeamArgs a, const Work work, int tiles) {
+    beam_merge_kernel(const BeamArgs a, const Work work, int pieces) {
   grid_dependency_wait();
   allow_dependents();
-  __shared__ uint64_t buffer[2 * kMergeCap];
-  merge_sequence<kMergeThreads>(a, work, tiles, blockIdx.x, buffer);
+  __shared__ struct {
+    __align__(16) double cs[kMergeCap];
+    __align__(16) int64_t cf[kMergeCap];
+    MergeShared<kMergeThreads / 32> merge;
+  } sh;
+  merge_sequence<kMergeThreads>(a, work, pieces, blockIdx.x, sh.merge, sh.cs, sh.cf);
 }
 
-// One tile of one row: kBeamThreads threads x LOADS 16-byte loads. MERGE: the CTA
-// of a sequence's last tile merges it.
+// Pieces of rows. A chunk is kBeamThreads threads x LOADS 16-byte loads of a row; a CTA
+// takes `per` chunks of the rows laid end to end and leaves a result for every row among
+// them. MERGE (one chunk a CTA): the CTA of a sequence's last piece merges it.
 template <typename T, int LOADS, bool MERGE>
 __global__ void __launch_bounds__(kBeamThreads, 4)
-    beam_tile_kernel(const BeamArgs a, const Work work, int tiles) {
+    beam_piece_kernel(const BeamArgs a, const Work work, int chunks, int per, int pieces) {
   grid_dependency_wait();
   allow_dependents();
   constexpr int EPL = Logits<T>::kPerLoad;
-  constexpr int kPer = EPL * LOADS;
+  constexpr int kChunk = kBeamThreads * EPL * LOADS;
   constexpr int kWarps = kBeamThreads / 32;
-  __shared__ __align__(16) uint32_t group_max[kGroups];
-  __shared__ float warp_max[kWarps], warp_sum[kWarps];
-  __shared__ uint64_t cand[kTileCap];
-  __shared__ uint32_t threshold;
-  __shared__ int count;
-  const int row = blockIdx.x / tiles, tile = blockIdx.x - row * tiles;
+  constexpr float kLog2e = 1.4426950408889634f;
+  struct Shared {
+    __align__(16) uint64_t cand[kPieceCap];
+    __align__(16) float chunk_max[MERGE ? 1 : kMaxPer][kBeamThreads];  // of each thread
+    __align__(16) uint32_t group_max[kGroups];
+    __align__(16) float warp_max[kWarps];
+    __align__(16) float warp_sum[kWarps];
+    __align__(16) uint32_t threshold;
+    int count, last_piece;
+  };
+  __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int vocab = a.vocab, select = a.select;
-  const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
-  const int base = tile * kBeamThreads * kPer;
-  // element e of load i of this thread: index base + (i * kBeamThreads + thread) EPL + e;
-  // past the row: -inf, which is never a candidate and adds nothing
-  auto load = [&](int at) {
-    if (at + EPL <= vocab) return __ldg(reinterpret_cast<const uint4*>(x + at));
-    float f[EPL];
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) f[e] = at + e < vocab ? Logits<T>::one(x + at + e) : -INFINITY;
-    return Logits<T>::narrow(f);
-  };
-  uint4 u[LOADS];
-  if (base + kBeamThreads * kPer <= vocab) {  // the whole tile: one address, no tests
-    const uint4* from = reinterpret_cast<const uint4*>(x + base) + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) u[i] = __ldg(from + i * kBeamThreads);
-  } else {
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i)
-      u[i] = load(base + (i * kBeamThreads + (int)threadIdx.x) * EPL);
-  }
-  if (threadIdx.x == 0) {
-    count = 0;
-    threshold = 0;
-  }
-  float load_max[LOADS];
-  float mx = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    load_max[i] = Logits<T>::largest(u[i]);
-    mx = fmaxf(mx, load_max[i]);
-  }
-  // groups of four neighbouring lanes
-  float gm = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
-  if ((lane & 3) == 0) group_max[threadIdx.x >> 2] = orderable(gm);
-  float wm = gm;
-#pragma unroll
-  for (int mask = 4; mask <= 16; mask <<= 1)
-    wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, mask));
-  __syncthreads();
-  {
-    // the select-th largest of the groups' maxima: the largest value with at least
-    // `select` maxima at or above it; four threads count for each group
-    const uint32_t g = group_max[threadIdx.x >> 2];
-    int rank = 0;
-#pragma unroll
-    for (int i = 0; i < kGroups / 4; i += 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(group_max + 4 * i + 4 * (lane & 3));
-      rank += (v.x >= g) + (v.y >= g) + (v.z >= g) + (v.w >= g);
+  const int total = a.num_seqs * a.num_beams * chunks;
+  int at_chunk = blockIdx.x * per;
+  const int end_chunk = min(at_chunk + per, total);
+  while (at_chunk < end_chunk) {
+    const int row = at_chunk / chunks, c0 = at_chunk - row * chunks;
+    const int n_chunks = MERGE ? 1 : min(end_chunk - at_chunk, chunks - c0);
+    const int piece = (int)blockIdx.x - row * chunks / per;
+    const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
+    const int begin = c0 * kChunk;
+    if (threadIdx.x == 0) {  // read behind the barriers below
+      sh.count = 0;
+      sh.threshold = 0;
     }
-    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
-    const uint32_t best = __reduce_max_sync(0xffffffffu, rank >= select ? g : 0u);
-    if (lane == 0) atomicMax(&threshold, best);
-  }
-  // sum of exponentials relative to the warp's maximum; a NaN makes it NaN
-  const float ref = wm == -INFINITY ? 0.f : wm;
-  constexpr float kLog2e = 1.4426950408889634f;
-  float even = 0.f, odd = 0.f;  // summed in pairs by packed fp32 instructions
+    // element e of load i of chunk j: index begin + j kChunk + (i kBeamThreads + thread) EPL
+    // + e; past the row: -inf, which is never a candidate and adds nothing
+    auto fetch = [&](uint4(&u)[LOADS], int j) {  // a chunk that the row covers
+      const uint4* from = reinterpret_cast<const uint4*>(x + begin + j * kChunk) + threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    float f[EPL];
-    Logits<T>::widen(u[i], f);
+      for (int i = 0; i < LOADS; ++i) u[i] = __ldg(from + i * kBeamThreads);
+    };
+    auto fetch_bounded = [&](uint4(&u)[LOADS], int j) {
 #pragma unroll
-    for (int e = 0; e < EPL; e += 2) {
-      // (x - ref) log2 e: the difference first, so that a row of the type's lowest or
-      // largest values is as exact as another
-      float p = f[e], q = f[e + 1];
-      fadd2(p, q, -ref, -ref);
-      fmul2(p, q, kLog2e);
-      fadd2(even, odd, fast_exp2(p), fast_exp2(q));
+      for (int i = 0; i < LOADS; ++i)
+        u[i] = load_bounded<T>(
+            x, begin + j * kChunk + (i * kBeamThreads + (int)threadIdx.x) * EPL, vocab);
+    };
+    const int whole = min(n_chunks, vocab / kChunk - c0);  // the row's last may be short
+    // the thread's largest logit and its sum of exponentials relative to it; a NaN makes
+    // the sum NaN
+    float mx = -INFINITY, sum = 0.f;
+    auto take = [&](const uint4(&u)[LOADS], int j) {
+      const float cm = Logits<T>::template largest<LOADS>(u);
+      sh.chunk_max[j][threadIdx.x] = cm;
+      const float to = fmaxf(mx, cm);
+      const float ref = to == -INFINITY ? 0.f : to;
+      const float keep = fast_exp2((mx - ref) * kLog2e);
+      mx = to;
+      float even = 0.f, odd = 0.f;  // summed in pairs by packed fp32 instructions
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        float f[EPL];
+        Logits<T>::widen(u[i], f);
+#pragma unroll
+        for (int e = 0; e < EPL; e += 2) {
+          // (x - ref) log2 e: the difference first, so that a row of the type's lowest or
+          // largest values is as exact as another
+          float p = f[e], q = f[e + 1];
+          fadd2(p, q, -ref, -ref);
+          fmul2(p, q, kLog2e);
+          fadd2(even, odd, fast_exp2(p), fast_exp2(q));
+        }
+      }
+      sum = fmaf(sum, keep, even + odd);
+    };
+    // a chunk's loads are on their way while the one before is taken; no barriers, so that
+    // warps drift apart and some always load
+    uint4 ua[LOADS];
+    if (whole > 0) {
+      fetch(ua, 0);
+      if constexpr (MERGE) {
+        take(ua, 0);
+      } else {
+        uint4 ub[LOADS];
+        for (int j = 0;;) {
+          fetch(ub, min(j + 1, whole - 1));
+          take(ua, j);
+          if (++j == whole) break;
+          fetch(ua, min(j + 1, whole - 1));
+          take(ub, j);
+          if (++j == whole) break;
+        }
+      }
     }
-  }
-  float sum = even + odd;
-#pragma unroll
-  for (int mask = 1; mask <= 16; mask <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mask);
-  if (lane == 0) {
-    warp_max[warp] = wm;
-    warp_sum[warp] = sum;
-  }
-  __syncthreads();
-  const float lowest = from_orderable(threshold);
-  // The few loads that hold candidates are read again (they are in L2): a loop over
-  // them is a fraction of the code that 64 tests in registers unroll to, and the
-  // instruction cache is what such code waits for.
-  uint32_t hits = 0;
-#pragma unroll
-  for (int i = 0; i < LOADS; ++i) hits |= (load_max[i] >= lowest ? 1u : 0u) << i;
-#pragma unroll 1
-  while (hits) {
-    const int i = __ffs(hits) - 1;
-    hits &= hits - 1;
-    const int at = base + (i * kBeamThreads + (int)threadIdx.x) * EPL;
-    float f[EPL];
-    Logits<T>::widen(load(at), f);
-    uint32_t in = 0;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) in |= (f[e] >= lowest && f[e] > -INFINITY ? 1u : 0u) << e;
-    int c = in ? atomicAdd(&count, __popc(in)) : 0;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e)
-      if ((in >> e) & 1u) {
-        if (c < kTileCap) cand[c] = make_key(f[e], at + e);
-        ++c;
-      }
-  }
-  const size_t out = (size_t)row * tiles + tile;
-  if (threadIdx.x == 0) {
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, warp_max[w]);
-    float S = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      S += warp_sum[w] * (warp_max[w] == -INFINITY
-                              ? 1.f
-                              : expf(warp_max[w] - M));
-    work.max[out] = M;
-    work.sum[out] = S;
-  }
-  __syncthreads();
-  uint64_t* keys = work.keys + out * select;
-  auto take_one_by_one = [&]() {
-    // more ties than the buffer holds: one at a time, each the largest below the last
-    uint64_t last = ~0ull;
-    uint64_t* best = cand;  // [kWarps]
-    const int end = min(vocab, base + kBeamThreads * kPer);
-    for (int r = 0; r < select; ++r) {
-      uint64_t k = 0;
-#pragma unroll 4
-      for (int at = base + (int)threadIdx.x; at < end; at += kBeamThreads) {
-        const float f = Logits<T>::one(x + at);
-        const uint64_t c = make_key(f, at);
-        if (f > -INFINITY && c < last && c > k) k = c;
-      }
-#pragma unroll
-      for (int mask = 16; mask > 0; mask >>= 1) {
-        const uint64_t o = __shfl_xor_sync(0xffffffffu, k, mask);
-        k = o > k ? o : k;
-      }
-      __syncthreads();
-      if (lane == 0) best[warp] = k;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) k = best[w] > k ? best[w] : k;
-      if (threadIdx.x == 0) keys[r] = k;
-      last = k;
+    if (whole < n_chunks) {
+      fetch_bounded(ua, n_chunks - 1);
+      take(ua, n_chunks - 1);
     }
-  };
-  const int n = count;
-  if (n <= kTileCap) {
-    for (int i = threadIdx.x; i < n; i += kBeamThreads) {
-      const uint64_t k = cand[i];
+    // groups of four neighbouring lanes
+    float gm = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
+    if ((lane & 3) == 0) sh.group_max[threadIdx.x >> 2] = orderable(gm);
+    float wm = gm;
+#pragma unroll
+    for (int mask = 4; mask <= 16; mask <<= 1)
+      wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, mask));
+    if (mx > -INFINITY) sum *= fast_exp2((mx - wm) * kLog2e);
+#pragma unroll
+    for (int mask = 1; mask <= 16; mask <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, mask);
+    if (lane == 0) {
+      sh.warp_max[warp] = wm;
+      sh.warp_sum[warp] = sum;
+    }
+    __syncthreads();
+    {
+      // the select-th largest of the groups' maxima: the largest value with at least
+      // `select` maxima at or above it; four threads count for each group
+      const uint32_t g = sh.group_max[threadIdx.x >> 2];
       int rank = 0;
-      for (int j = 0; j < n; ++j) rank += cand[j] > k;
-      if (rank < select) keys[rank] = k;
-    }
-    for (int i = n + threadIdx.x; i < select; i += kBeamThreads) keys[i] = 0;
-  } else {
-    take_one_by_one();
-  }
-
-  if constexpr (MERGE) {
-    // as the split-KV merge of the decode: the barrier makes the CTA's stores visible to
-    // thread 0, whose gpu-scope acq_rel add publishes them
-    __shared__ bool last_tile;
-    const int seq = row / a.num_beams;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      last_tile = atom_add_acq_rel_gpu(work.done + seq, 1) == a.num_beams * tiles - 1;
-      if (last_tile) work.done[seq] = 0;
+#pragma unroll
+      for (int i = 0; i < kGroups / 4; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(sh.group_max + 4 * i + 4 * (lane & 3));
+        rank += (v.x >= g) + (v.y >= g) + (v.z >= g) + (v.w >= g);
+      }
+      rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+      rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+      const uint32_t best = __reduce_max_sync(0xffffffffu, rank >= select ? g : 0u);
+      if (lane == 0) atomicMax(&sh.threshold, best);
     }
     __syncthreads();
-    if (last_tile) merge_sequence<kBeamThreads>(a, work, tiles, seq, cand);
+    const size_t out = (size_t)row * pieces + piece;
+    if (warp == kWarps - 1) {  // lane w: warp w's share
+      const float m = lane < kWarps ? sh.warp_max[lane] : -INFINITY;
+      float S = lane < kWarps ? sh.warp_sum[lane] : 0.f;
+      float M = m;
+#pragma unroll
+      for (int mask = 1; mask < kWarps; mask <<= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, mask));
+      if (m > -INFINITY) S *= expf(m - M);
+#pragma unroll
+      for (int mask = 1; mask < kWarps; mask <<= 1) S += __shfl_xor_sync(0xffffffffu, S, mask);
+      if (lane == 0) {
+        work.max[out] = M;
+        work.sum[out] = S;
+      }
+    }
+    const float lowest = from_orderable(sh.threshold);
+    if constexpr (MERGE) {  // the one chunk is still in registers
+      if (mx >= lowest && mx > -INFINITY) {
+        uint32_t in = 0;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+          float f[EPL];
+          Logits<T>::widen(ua[i], f);
+#pragma unroll
+          for (int e = 0; e < EPL; ++e)
+            in |= (f[e] >= lowest && f[e] > -INFINITY ? 1u : 0u) << (i * EPL + e);
+        }
+        int c = atomicAdd(&sh.count, __popc(in));
+        for (; in; in &= in - 1, ++c) {
+          const int b = __ffs(in) - 1;
+          const int at = begin + (b / EPL * kBeamThreads + (int)threadIdx.x) * EPL + b % EPL;
+          if (c < kPieceCap) sh.cand[c] = make_key(Logits<T>::one(x + at), at);
+        }
+      }
+    } else {
+      // The few chunks of a thread that hold candidates are read again (from L2, mostly), the
+      // LOADS x EPL elements of one by a warp at once, two on their way together.
+      uint32_t hits = 0;
+#pragma unroll 4
+      for (int j = 0; j < n_chunks; ++j) {
+        const float cm = sh.chunk_max[j][threadIdx.x];
+        hits |= (cm >= lowest && cm > -INFINITY ? 1u : 0u) << j;
+      }
+      const int place = lane / EPL * kBeamThreads * EPL + lane % EPL;
+      for (uint32_t m; (m = __ballot_sync(0xffffffffu, hits != 0)) != 0;) {
+        const int first = __ffs(hits) - 1;  // -1 where there is none: not looked at
+        int at[2];
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int from = m ? __ffs(m) - 1 : 0;
+          const int j = __shfl_sync(0xffffffffu, first, from);
+          at[h] = begin + j * kChunk + (warp * 32 + from) * EPL + place;
+          f[h] = m != 0 && lane < LOADS * EPL && at[h] < vocab ? Logits<T>::one(x + at[h])
+                                                               : -INFINITY;
+          if (m != 0 && lane == from) hits &= hits - 1;
+          m &= m - 1;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (f[h] >= lowest && f[h] > -INFINITY) {
+            const int c = atomicAdd(&sh.count, 1);
+            if (c < kPieceCap) sh.cand[c] = make_key(f[h], at[h]);
+          }
+      }
+    }
+    __syncthreads();
+    uint64_t* keys = work.keys + out * select;
+    auto take_one_by_one = [&]() {
+      // more ties than the buffer holds: one at a time, each the largest below the last
+      uint64_t last = ~0ull;
+      uint64_t* best = sh.cand;  // [kWarps]
+      const int end = min(vocab, begin + n_chunks * kChunk);
+      for (int r = 0; r < select; ++r) {
+        uint64_t k = 0;
+#pragma unroll 4
+        for (int at = begin + (int)threadIdx.x; at < end; at += kBeamThreads) {
+          const float f = Logits<T>::one(x + at);
+          const uint64_t c = make_key(f, at);
+          if (f > -INFINITY && c < last && c > k) k = c;
+        }
+#pragma unroll
+        for (int mask = 16; mask > 0; mask >>= 1) {
+          const uint64_t o = __shfl_xor_sync(0xffffffffu, k, mask);
+          k = o > k ? o : k;
+        }
+        __syncthreads();
+        if (lane == 0) best[warp] = k;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) k = best[w] > k ? best[w] : k;
+        if (threadIdx.x == 0) keys[r] = k;
+        last = k;
+      }
+    };
+    const int n = sh.count;
+    if (n <= kPieceCap) {
+      for (int i = threadIdx.x; i < n; i += kBeamThreads) {
+        const uint64_t k = sh.cand[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += sh.cand[j] > k;
+        if (rank < select) keys[rank] = k;
+      }
+      for (int i = n + threadIdx.x; i < select; i += kBeamThreads) keys[i] = 0;
+    } else {
+      take_one_by_one();
+    }
+    if (c0 + n_chunks == chunks) {  // the row's last piece: the places that it has no piece for
+      for (int p = piece + 1; p < pieces; ++p) {
+        const size_t none = (size_t)row * pieces + p;
+        if (threadIdx.x == 0) {
+          work.max[none] = -INFINITY;
+          work.sum[none] = 0.f;
+        }
+        for (int i = threadIdx.x; i < select; i += kBeamThreads) work.keys[none * select + i] = 0;
+      }
+    }
+    if constexpr (MERGE) {
+      // as the split-KV merge of the decode: the barrier makes the CTA's stores visible to
+      // thread 0, whose gpu-scope acq_rel add publishes them
+      const int seq = row / a.num_beams;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        sh.last_piece = atom_add_acq_rel_gpu(work.done + seq, 1) == a.num_beams * pieces - 1;
+        if (sh.last_piece) work.done[seq] = 0;
+      }
+      __syncthreads();
+      if (sh.last_piece) {
+        static_assert(kPieceCap >= 2 * kMergeCap, "the merge takes the candidates' place");
+        __shared__ MergeShared<kWarps> merge;
+        merge_sequence<kBeamThreads>(a, work, pieces, seq, merge,
+                                     reinterpret_cast<double*>(sh.cand),
+                                     reinterpret_cast<int64_t*>(sh.cand + kMergeCap));
+      }
+      return;
+    }
+    at_chunk += n_chunks;
+    __syncthreads();  // the next row's piece uses the same shared memory
   }
 }
 
-// Elements of a tile: 64 per thread (16-bit) or 32 (fp32) for large work, a
-// quarter for little.
-template <typename T>
-constexpr int tile_elems(bool large) {
-  return kBeamThreads * Logits<T>::kPerLoad * (large ? 8 : 2);
-}
+// Little work: a chunk of kSmallLoads loads a thread per CTA, merged in the same launch.
+// Much: chunks of kLargeLoads, shared out evenly over the CTAs that the SMs hold at once.
+constexpr int kSmallLoads = 2, kLargeLoads = 4;
+constexpr int kResident = 148 * 4;
+static_assert(kLargeLoads * 8 <= 32, "a warp reads a thread's chunk at once");
 
-constexpr int kLargeTiles = 148 * 2;
-
-bool large_tiles(int64_t rows, int vocab, int elem) {
-  // enough large tiles for every SM to hold two CTAs
-  const int64_t big = elem == 4 ? tile_elems<float>(true) : tile_elems<__half>(true);
-  return rows * ((vocab + big - 1) / big) >= kLargeTiles;
+int chunks_of(int vocab, int elem, int loads) {
+  const int chunk = kBeamThreads * (16 / elem) * loads;
+  return (vocab + chunk - 1) / chunk;
 }
 
 }  // namespace
@@ -535,15 +643,23 @@ bool large_tiles(int64_t rows, int vocab, int elem) {
 void beam_layout(int num_seqs, int num_beams, int vocab, int select, int dtype, BeamLayout* lay) {
   const int elem = dtype == PA_F32 ? 4 : 2;
   const int64_t rows = (int64_t)num_seqs * num_beams;
-  const bool large = large_tiles(rows, vocab, elem);
-  const int64_t per = elem == 4 ? tile_elems<float>(large) : tile_elems<__half>(large);
-  lay->large = large;
-  lay->tiles = (int)((vocab + per - 1) / per);
+  lay->chunks = chunks_of(vocab, elem, kLargeLoads);
+  lay->large = rows * lay->chunks >= kResident;
+  lay->per = 1;
+  if (lay->large) {
+    const int64_t total = rows * lay->chunks, once = (int64_t)kResident * kMaxPer;
+    const int64_t slots = (total + once - 1) / once * kResident;
+    lay->per = (int)((total + slots - 1) / slots);
+  } else {
+    lay->chunks = chunks_of(vocab, elem, kSmallLoads);
+  }
+  // a row that starts inside a CTA's share
+  lay->pieces = (lay->chunks + lay->per - 2) / lay->per + 1;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t n = (size_t)rows * lay->tiles;
-  // small tiles only come with fewer sequences than kLargeTiles; the counters have a place
+  const size_t n = (size_t)rows * lay->pieces;
+  // little work only comes with fewer sequences than kResident; the counters have a place
   // of their own whatever the sizes, so that no call leaves results where another counts
-  lay->max_off = up(kLargeTiles * sizeof(int));
+  lay->max_off = up(kResident * sizeof(int));
   lay->sum_off = lay->max_off + up(n * sizeof(float));
   lay->key_off = lay->sum_off + up(n * sizeof(float));
   lay->bytes = lay->key_off + up(n * select * sizeof(uint64_t));
@@ -558,23 +674,25 @@ cudaError_t launch_beam_select(const BeamArgs& a, int dtype, cudaStream_t stream
   work.max = reinterpret_cast<float*>(ws + lay.max_off);
   work.sum = reinterpret_cast<float*>(ws + lay.sum_off);
   work.keys = reinterpret_cast<uint64_t*>(ws + lay.key_off);
-  const int64_t ctas = (int64_t)lay.tiles * a.num_seqs * a.num_beams;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int64_t total = (int64_t)lay.chunks * a.num_seqs * a.num_beams;
+  if (total > 0x7fff0000LL) return cudaErrorInvalidValue;
   auto go = [&](auto kern) {
-    return launch_dependent(kern, dim3((unsigned)ctas), dim3(kBeamThreads), 0, stream, a, work,
-                            lay.tiles);
+    return launch_dependent(kern, dim3((unsigned)((total + lay.per - 1) / lay.per)),
+                            dim3(kBeamThreads), 0, stream, a, work, lay.chunks, lay.per,
+                            lay.pieces);
   };
   if (!lay.large) {
-    return dtype == PA_F32   ? go(beam_tile_kernel<float, 2, true>)
-           : dtype == PA_F16 ? go(beam_tile_kernel<__half, 2, true>)
-                             : go(beam_tile_kernel<__nv_bfloat16, 2, true>);
+    return dtype == PA_F32   ? go(beam_piece_kernel<float, kSmallLoads, true>)
+           : dtype == PA_F16 ? go(beam_piece_kernel<__half, kSmallLoads, true>)
+                             : go(beam_piece_kernel<__nv_bfloat16, kSmallLoads, true>);
   }
-  const cudaError_t e = dtype == PA_F32   ? go(beam_tile_kernel<float, 8, false>)
-                        : dtype == PA_F16 ? go(beam_tile_kernel<__half, 8, false>)
-                                          : go(beam_tile_kernel<__nv_bfloat16, 8, false>);
+  const cudaError_t e = dtype == PA_F32 ? go(beam_piece_kernel<float, kLargeLoads, false>)
+                        : dtype == PA_F16
+                            ? go(beam_piece_kernel<__half, kLargeLoads, false>)
+                            : go(beam_piece_kernel<__nv_bfloat16, kLargeLoads, false>);
   if (e != cudaSuccess) return e;
   return launch_dependent(beam_merge_kernel, dim3(a.num_seqs), dim3(kMergeThreads), 0, stream, a,
-                          work, lay.tiles);
+                          work, lay.pieces);
 }
 
 }  // namespace pa

@@ -1149,8 +1149,8 @@ static int check_beam_sizes(int num_seqs, int num_beams, int vocab, int num_sele
     return fail(PA_ERR_UNSUPPORTED, "vocab %d: expected 1 .. 2^24", vocab);
   BeamLayout lay;
   beam_layout(num_seqs, num_beams, vocab, num_select, dtype, &lay);
-  if ((long long)num_seqs * num_beams * lay.tiles > 0x7fff0000LL)  // tiles count in an int
-    return fail(PA_ERR_UNSUPPORTED, "num_seqs x num_beams x vocab: too many tiles");
+  if ((long long)num_seqs * num_beams * lay.chunks > 0x7fff0000LL)  // chunks count in an int
+    return fail(PA_ERR_UNSUPPORTED, "num_seqs x num_beams x vocab: too many chunks");
   return PA_OK;
 }
 

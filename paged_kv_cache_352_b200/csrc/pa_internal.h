@@ -199,8 +199,10 @@ struct BeamArgs {
 // Workspace: counters of sequences, then per (row, tile) a maximum, a sum of
 // exponentials and `select` keys.
 struct BeamLayout {
-  bool large;  // tile size
-  int tiles;   // tiles per row
+  bool large;  // chunk size
+  int chunks;  // chunks per row
+  int per;     // chunks per CTA
+  int pieces;  // results per row, at most
   size_t max_off, sum_off, key_off, bytes;
 };
 void beam_layout(int num_seqs, int num_beams, int vocab, int select, int dtype, BeamLayout* lay);
