@@ -5,25 +5,32 @@
 //   the N largest of the K V scores of a sequence, ties to the smallest k V + v.
 //
 // The logits are read once: 2 or 4 bytes each, against one exponential, a
-// comparison and an addition. A row's ranking does not need its logsumexp, so one
-// CTA takes a tile of a row (kept in registers) and leaves the tile's maximum, its
-// sum of exponentials and its N largest logits in the workspace; then one CTA per
-// sequence adds up the rows' sums and ranks K x tiles x N candidates. For little
-// work that is the CTA that finishes the sequence's last tile (4 beams of 32000
-// logits: 10.3 us a call instead of 12.9 us with a second launch); for much work it
-// is a second launch, since every tile would wait for the release of its results
-// (64 x 8 beams of 131072 logits: 41.8 us instead of 47.6 us).
+// comparison and an addition. A row's ranking does not need its logsumexp, so a CTA
+// takes a piece of a row and leaves the piece's maximum, its sum of exponentials and
+// its N largest logits in the workspace; then one CTA per sequence adds up the rows'
+// sums and ranks K x pieces x N candidates. For little work a piece is 8 or 16 logits a
+// thread and the CTA that finishes the sequence's last piece merges it (4 beams of 32000
+// logits: 6.7 us; a second launch cost 2.6 us more). For much work 4 CTAs an SM each walk
+// an equal share of the rows laid end to end, as pieces of up to 16 chunks, and a second
+// launch merges: its launch is cheaper than every CTA's wait for the release of its
+// results. 64 x 8 beams of 131072 bf16 logits take 37.3 us, 31 of them reading (20.8 at
+// the copy rate); 41.1 us with a CTA and a piece per 16384 logits, 41.3 and 42.5 us with
+// shares of at most 8 and 4 chunks, 40.9 us with chunks copied two ahead through shared
+// memory (fewer waits, more instructions), 43.2 us with 3 CTAs an SM. What is left is
+// spread over the exponentials (half of their pipe's rate), issue (45 %), the ends of the
+// pieces and SMs that finish 10 % apart.
 //
-// The N largest of a tile without sorting it: the N-th largest of the maxima of
-// kGroups groups of elements bounds the N-th largest element from below, so the few
+// The N largest of a piece without sorting it: the N-th largest of the maxima of
+// kGroups groups of threads bounds the N-th largest element from below, so the few
 // elements at or above it are collected in shared memory and ranked by counting,
-// for each, those before it. Where ties make too many (a tile of equal logits) the N
+// for each, those before it. Where ties make too many (a piece of equal logits) the N
 // are taken one by one instead; either way the order is (value descending, index
 // ascending), and a result does not depend on the order of the atomics.
 //
 // Scores are formed and ranked in double precision: neighbouring candidates of
-// different beams are often closer than fp32 scores resolve. The exponentials'
-// sums are fp32 per thread (at most kPer terms), double from there on.
+// different beams are often closer than fp32 scores resolve. The exponentials' sums are
+// fp32 per chunk and thread (at most 32 terms), per piece (at most 16 chunks) and CTA,
+// double from there on.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <string.h>
@@ -37,8 +44,8 @@ namespace pa {
 namespace {
 
 constexpr int kBeamThreads = 256;
-constexpr int kGroups = 64;       // groups of a tile whose maxima bound the N-th largest
-constexpr int kPieceCap = 2048;    // candidates a piece ranks at once
+constexpr int kGroups = 64;       // groups of a piece whose maxima bound the N-th largest
+constexpr int kPieceCap = 2048;   // candidates a piece ranks at once
 constexpr int kMergeCap = 1024;   // candidates a sequence ranks at once
 constexpr int kMaxPer = 16;       // chunks of a CTA's share
 
@@ -57,8 +64,8 @@ __device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
   return ((uint64_t)orderable(__fadd_rn(x, 0.f)) << 32) | (uint32_t)~index;
 }
 
-// A 16-byte load of logits: kPerLoad of them, kept packed in registers (a tile of
-// 64 16-bit logits a thread is 32 registers, and four CTAs fit an SM).
+// A 16-byte load of logits: kPerLoad of them, kept packed in registers (two chunks of
+// 16-bit logits, one taken and one on its way, are 32: four CTAs fit an SM).
 template <typename T>
 struct Logits {
   static constexpr int kPerLoad = 8;
@@ -115,12 +122,11 @@ struct Logits<float> {
   }
 };
 
-// The 16 bytes of logits at `at`, -inf past the row. Called for a row's last chunk and
-// for candidates only: out of the way of the loop over whole chunks.
+// The 16 bytes of logits at `at`, -inf past the row: the end of a row and what lies
+// behind it in its last chunk.
 template <typename T>
-__device__ __noinline__ uint4 load_bounded(const T* x, int at, int vocab) {
+__device__ __noinline__ uint4 load_last(const T* x, int at, int vocab) {
   constexpr int EPL = Logits<T>::kPerLoad;
-  if (at + EPL <= vocab) return __ldg(reinterpret_cast<const uint4*>(x + at));
   float f[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) f[e] = at + e < vocab ? Logits<T>::one(x + at + e) : -INFINITY;
@@ -129,14 +135,14 @@ __device__ __noinline__ uint4 load_bounded(const T* x, int at, int vocab) {
 
 // The workspace's parts.
 struct Work {
-  int* done;       // [num_seqs] tiles finished, back to 0 after the merge (small tiles)
-  float* max;      // [rows][tiles]
-  float* sum;      // [rows][tiles]
-  uint64_t* keys;  // [rows][tiles][select], best first, 0 past the candidates
+  int* done;       // [num_seqs] pieces finished, back to 0 after the merge (little work)
+  float* max;      // [rows][pieces]
+  float* sum;      // [rows][pieces], of the exponentials relative to max
+  uint64_t* keys;  // [rows][pieces][select], best first, 0 past the candidates
 };
 
 // Candidates are ordered by score, ties to the smaller flat index.
-__device__ __forceinline__ bool before(double s, int64_t f, double t, int64_t g) {
+__device__ __forceinline__ bool before(double s, int32_t f, double t, int32_t g) {
   return s > t || (s == t && f < g);
 }
 
@@ -150,7 +156,7 @@ struct MergeShared {
   __align__(16) double group_max[kGroups];
   __align__(16) double warp_best[kWarps];
   __align__(16) double best_score[kWarps];
-  __align__(16) int64_t best_index[kWarps];
+  __align__(16) int32_t best_index[kWarps];
   __align__(16) int count;
 };
 
@@ -160,7 +166,7 @@ struct MergeShared {
 template <int kMergeThreads>
 __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& work, int pieces,
                                                int b, MergeShared<kMergeThreads / 32>& sh,
-                                               double* cs, int64_t* cf) {
+                                               double* cs, int32_t* cf) {
   constexpr int kWarps = kMergeThreads / 32;
   const int beams = a.num_beams, vocab = a.vocab, select = a.select;
   const float* piece_max = work.max;
@@ -179,19 +185,26 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
   }
   for (int k = warp; k < beams; k += kWarps) {
     const size_t row = (size_t)b * beams + k;
-    float M = -INFINITY;
-    for (int t = lane; t < pieces; t += 32) M = fmaxf(M, __ldcg(piece_max + row * pieces + t));
+    float m0 = -INFINITY, s0 = 0.f;  // the first 32 pieces stay in registers
+    if (lane < pieces) {
+      m0 = __ldcg(piece_max + row * pieces + lane);
+      s0 = __ldcg(piece_sum + row * pieces + lane);
+    }
+    const float beam = lane == 0 ? a.beam_scores[row] : 0.f;
+    float M = m0;
+    for (int t = lane + 32; t < pieces; t += 32) M = fmaxf(M, __ldcg(piece_max + row * pieces + t));
 #pragma unroll
     for (int mask = 16; mask > 0; mask >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, mask));
     double S = 0.0;
-    for (int t = lane; t < pieces; t += 32) {
-      const float m = __ldcg(piece_max + row * pieces + t), s = __ldcg(piece_sum + row * pieces + t);
+    auto add = [&](float m, float s) {
       if (m > -INFINITY || s != s) S += (double)s * exp((double)m - (double)M);
-    }
+    };
+    add(m0, s0);
+    for (int t = lane + 32; t < pieces; t += 32)
+      add(__ldcg(piece_max + row * pieces + t), __ldcg(piece_sum + row * pieces + t));
 #pragma unroll
     for (int mask = 16; mask > 0; mask >>= 1) S += __shfl_xor_sync(0xffffffffu, S, mask);
     if (lane == 0) {
-      const float beam = a.beam_scores[row];
       double o = -INFINITY;
       if (M > -INFINITY || S != S) o = M < INFINITY ? (double)beam - log(S) : NAN;
       if (o != o || o == INFINITY) {  // a NaN or +inf among the logits, or as beam score
@@ -204,22 +217,22 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
   }
   if (threadIdx.x == 0) sh.count = 0;
   __syncthreads();
-  auto score_key = [&](int i, uint64_t key, double& s, int64_t& f) {
+  auto score_key = [&](int i, uint64_t key, double& s, int32_t& f) {
     const int k = i / per_beam;
     s = -INFINITY;
-    f = INT64_MAX;
+    f = INT32_MAX;
     if (key != 0 && sh.offset[k] > -INFINITY) {
       s = ((double)from_orderable((uint32_t)(key >> 32)) - (double)sh.largest[k]) + sh.offset[k];
-      f = (int64_t)k * vocab + (uint32_t)~(uint32_t)key;
+      f = k * vocab + (int32_t)~(uint32_t)key;  // below 2^30
     }
   };
-  auto score_of = [&](int i, double& s, int64_t& f) {
+  auto score_of = [&](int i, double& s, int32_t& f) {
     score_key(i, __ldcg(piece_keys + (size_t)b * total + i), s, f);
   };
   // as in a piece: the select-th largest of 64 groups' maxima bounds the result from below
   double top = -INFINITY;
   double as[kAhead];
-  int64_t af[kAhead];
+  int32_t af[kAhead];
 #pragma unroll
   for (int j = 0; j < kAhead; ++j) {
     as[j] = -INFINITY;
@@ -229,7 +242,7 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
   }
   for (int i = threadIdx.x + kAhead * kMergeThreads; i < total; i += kMergeThreads) {
     double s;
-    int64_t f;
+    int32_t f;
     score_of(i, s, f);
     top = s > top ? s : top;
   }
@@ -261,7 +274,7 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
   double lowest = sh.warp_best[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) lowest = sh.warp_best[w] > lowest ? sh.warp_best[w] : lowest;
-  auto collect = [&](double s, int64_t f) {
+  auto collect = [&](double s, int32_t f) {
     if (s > -INFINITY && s >= lowest) {
       const int at = atomicAdd(&sh.count, 1);
       if (at < kMergeCap) {
@@ -274,22 +287,22 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
   for (int j = 0; j < kAhead; ++j) collect(as[j], af[j]);
   for (int i = threadIdx.x + kAhead * kMergeThreads; i < total; i += kMergeThreads) {
     double s;
-    int64_t f;
+    int32_t f;
     score_of(i, s, f);
     collect(s, f);
   }
   __syncthreads();
   const int n = sh.count;
   const size_t out = (size_t)b * select;
-  auto put = [&](int rank, double s, int64_t f) {
+  auto put = [&](int rank, double s, int32_t f) {
     a.scores[out + rank] = (float)s;
-    a.parents[out + rank] = s > -INFINITY ? (int32_t)(f / vocab) : -1;
-    a.tokens[out + rank] = s > -INFINITY ? (int32_t)(f % vocab) : -1;
+    a.parents[out + rank] = s > -INFINITY ? f / vocab : -1;
+    a.tokens[out + rank] = s > -INFINITY ? f % vocab : -1;
   };
   if (n <= kMergeCap) {
     for (int i = threadIdx.x; i < n; i += kMergeThreads) {
       const double s = cs[i];
-      const int64_t f = cf[i];
+      const int32_t f = cf[i];
       int rank = 0;
       for (int j = 0; j < n; ++j) rank += before(cs[j], cf[j], s, f);
       if (rank < select) put(rank, s, f);
@@ -299,13 +312,13 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
   }
   // more equal candidates than the buffer holds: one at a time
   double ls = INFINITY;
-  int64_t lf = -1;
+  int32_t lf = -1;
   for (int r = 0; r < select; ++r) {
     double s = -INFINITY;
-    int64_t f = INT64_MAX;
+    int32_t f = INT32_MAX;
     for (int i = threadIdx.x; i < total; i += kMergeThreads) {
       double t;
-      int64_t g;
+      int32_t g;
       score_of(i, t, g);
       if (t > -INFINITY && before(ls, lf, t, g) && before(t, g, s, f)) {
         s = t;
@@ -315,7 +328,7 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
 #pragma unroll
     for (int mask = 16; mask > 0; mask >>= 1) {
       const double t = __shfl_xor_sync(0xffffffffu, s, mask);
-      const int64_t g = __shfl_xor_sync(0xffffffffu, f, mask);
+      const int32_t g = __shfl_xor_sync(0xffffffffu, f, mask);
       if (before(t, g, s, f)) {
         s = t;
         f = g;
@@ -340,13 +353,13 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
 
 constexpr int kMergeThreads = 512;
 
-__global__ void __launch_bounds__(kMergeThreads)
+__global__ void __launch_bounds__(kMergeThreads, 1)
     beam_merge_kernel(const BeamArgs a, const Work work, int pieces) {
   grid_dependency_wait();
   allow_dependents();
   __shared__ struct {
     __align__(16) double cs[kMergeCap];
-    __align__(16) int64_t cf[kMergeCap];
+    __align__(16) int32_t cf[kMergeCap];
     MergeShared<kMergeThreads / 32> merge;
   } sh;
   merge_sequence<kMergeThreads>(a, work, pieces, blockIdx.x, sh.merge, sh.cs, sh.cf);
@@ -354,10 +367,12 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 // Pieces of rows. A chunk is kBeamThreads threads x LOADS 16-byte loads of a row; a CTA
 // takes `per` chunks of the rows laid end to end and leaves a result for every row among
-// them. MERGE (one chunk a CTA): the CTA of a sequence's last piece merges it.
+// them, or with by_rows `per` chunks of one row. MERGE (one chunk a CTA): the CTA of a
+// sequence's last piece merges it.
 template <typename T, int LOADS, bool MERGE>
 __global__ void __launch_bounds__(kBeamThreads, 4)
-    beam_piece_kernel(const BeamArgs a, const Work work, int chunks, int per, int pieces) {
+    beam_piece_kernel(const BeamArgs a, const Work work, int chunks, int per, int pieces,
+                      bool by_rows) {
   grid_dependency_wait();
   allow_dependents();
   constexpr int EPL = Logits<T>::kPerLoad;
@@ -377,12 +392,19 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int vocab = a.vocab, select = a.select;
   const int total = a.num_seqs * a.num_beams * chunks;
-  int at_chunk = blockIdx.x * per;
-  const int end_chunk = min(at_chunk + per, total);
+  int at_chunk, end_chunk;
+  if (by_rows) {
+    const int row = blockIdx.x / pieces;
+    at_chunk = row * chunks + ((int)blockIdx.x - row * pieces) * per;
+    end_chunk = min(at_chunk + per, (row + 1) * chunks);
+  } else {
+    at_chunk = blockIdx.x * per;
+    end_chunk = min(at_chunk + per, total);
+  }
   while (at_chunk < end_chunk) {
     const int row = at_chunk / chunks, c0 = at_chunk - row * chunks;
     const int n_chunks = MERGE ? 1 : min(end_chunk - at_chunk, chunks - c0);
-    const int piece = (int)blockIdx.x - row * chunks / per;
+    const int piece = (int)blockIdx.x - (by_rows ? row * pieces : row * chunks / per);
     const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.row_stride;
     const int begin = c0 * kChunk;
     if (threadIdx.x == 0) {  // read behind the barriers below
@@ -397,10 +419,17 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
       for (int i = 0; i < LOADS; ++i) u[i] = __ldg(from + i * kBeamThreads);
     };
     auto fetch_bounded = [&](uint4(&u)[LOADS], int j) {
+      const int base = begin + j * kChunk + (int)threadIdx.x * EPL;
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i)
-        u[i] = load_bounded<T>(
-            x, begin + j * kChunk + (i * kBeamThreads + (int)threadIdx.x) * EPL, vocab);
+      for (int i = 0; i < LOADS; ++i) {
+        const int at = base + i * kBeamThreads * EPL;
+        if (at + EPL <= vocab) u[i] = __ldg(reinterpret_cast<const uint4*>(x + at));
+      }
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int at = base + i * kBeamThreads * EPL;
+        if (at + EPL > vocab) u[i] = load_last<T>(x, at, vocab);
+      }
     };
     const int whole = min(n_chunks, vocab / kChunk - c0);  // the row's last may be short
     // the thread's largest logit and its sum of exponentials relative to it; a NaN makes
@@ -618,7 +647,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
         __shared__ MergeShared<kWarps> merge;
         merge_sequence<kBeamThreads>(a, work, pieces, seq, merge,
                                      reinterpret_cast<double*>(sh.cand),
-                                     reinterpret_cast<int64_t*>(sh.cand + kMergeCap));
+                                     reinterpret_cast<int32_t*>(sh.cand + kMergeCap));
       }
       return;
     }
@@ -631,6 +660,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
 // Much: chunks of kLargeLoads, shared out evenly over the CTAs that the SMs hold at once.
 constexpr int kSmallLoads = 2, kLargeLoads = 4;
 constexpr int kResident = 148 * 4;
+constexpr int kCounters = 512;  // sequences whose pieces are counted (little work)
 static_assert(kLargeLoads * 8 <= 32, "a warp reads a thread's chunk at once");
 
 int chunks_of(int vocab, int elem, int loads) {
@@ -644,7 +674,7 @@ void beam_layout(int num_seqs, int num_beams, int vocab, int select, int dtype, 
   const int elem = dtype == PA_F32 ? 4 : 2;
   const int64_t rows = (int64_t)num_seqs * num_beams;
   lay->chunks = chunks_of(vocab, elem, kLargeLoads);
-  lay->large = rows * lay->chunks >= kResident;
+  lay->large = rows * lay->chunks >= kResident || num_seqs > kCounters;
   lay->per = 1;
   if (lay->large) {
     const int64_t total = rows * lay->chunks, once = (int64_t)kResident * kMaxPer;
@@ -653,13 +683,16 @@ void beam_layout(int num_seqs, int num_beams, int vocab, int select, int dtype, 
   } else {
     lay->chunks = chunks_of(vocab, elem, kSmallLoads);
   }
-  // a row that starts inside a CTA's share
-  lay->pieces = (lay->chunks + lay->per - 2) / lay->per + 1;
+  lay->pieces = (lay->chunks + lay->per - 1) / lay->per;
+  // Shares of one row each while they fit the SMs at once, too: a CTA then ends one piece, not
+  // two (16 x 4 beams of 50257 fp32 logits: 9.3 us instead of 10.3 us).
+  lay->by_rows = rows * lay->pieces <= kResident || !lay->large;
+  if (!lay->by_rows) lay->pieces = (lay->chunks + lay->per - 2) / lay->per + 1;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t n = (size_t)rows * lay->pieces;
-  // little work only comes with fewer sequences than kResident; the counters have a place
-  // of their own whatever the sizes, so that no call leaves results where another counts
-  lay->max_off = up(kResident * sizeof(int));
+  // the counters have a place of their own whatever the sizes, so that no call leaves results
+  // where another counts
+  lay->max_off = up(kCounters * sizeof(int));
   lay->sum_off = lay->max_off + up(n * sizeof(float));
   lay->key_off = lay->sum_off + up(n * sizeof(float));
   lay->bytes = lay->key_off + up(n * select * sizeof(uint64_t));
@@ -677,9 +710,10 @@ cudaError_t launch_beam_select(const BeamArgs& a, int dtype, cudaStream_t stream
   const int64_t total = (int64_t)lay.chunks * a.num_seqs * a.num_beams;
   if (total > 0x7fff0000LL) return cudaErrorInvalidValue;
   auto go = [&](auto kern) {
-    return launch_dependent(kern, dim3((unsigned)((total + lay.per - 1) / lay.per)),
-                            dim3(kBeamThreads), 0, stream, a, work, lay.chunks, lay.per,
-                            lay.pieces);
+    const int64_t ctas = lay.by_rows ? (int64_t)lay.pieces * a.num_seqs * a.num_beams
+                                     : (total + lay.per - 1) / lay.per;
+    return launch_dependent(kern, dim3((unsigned)ctas), dim3(kBeamThreads), 0, stream, a, work,
+                            lay.chunks, lay.per, lay.pieces, lay.by_rows);
   };
   if (!lay.large) {
     return dtype == PA_F32   ? go(beam_piece_kernel<float, kSmallLoads, true>)

@@ -35,6 +35,11 @@
 //   - a step takes two blocks: one vote, one wait for 32 tokens, and two
 //     independent chains of products.
 //
+// Measured: 64 sequences of 128-2048 tokens, 32 heads, d = 128, f16 (337 MB): 66 us,
+// 5.1 TB/s; the other caches' loop over these tiles took 105.5 us, the same loads without
+// arithmetic take 53.9 us, a copy of the bytes 52.1 us. 8 sequences of 32768-131072 tokens,
+// 64 query and 8 KV heads, bf16: 131 us (loads alone 114).
+//
 // S = K Q^T. Lane 4g + c holds k-slots 2c, 2c+1, 2c+8, 2c+9 of A (rows g, g + 8)
 // and of B (column g). It takes dimensions 8W c .. 8W c + 8W - 1 (W = d/32 words a
 // row) of tokens g and g + 8, and of query head g: word j of a row gives two

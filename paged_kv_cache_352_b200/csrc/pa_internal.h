@@ -196,13 +196,14 @@ struct BeamArgs {
   void* workspace;
   int* dev_error;
 };
-// Workspace: counters of sequences, then per (row, tile) a maximum, a sum of
+// Workspace: counters of sequences, then per (row, piece) a maximum, a sum of
 // exponentials and `select` keys.
 struct BeamLayout {
-  bool large;  // chunk size
-  int chunks;  // chunks per row
-  int per;     // chunks per CTA
-  int pieces;  // results per row, at most
+  bool large;    // chunk size
+  int chunks;    // chunks per row
+  int per;       // chunks per CTA
+  int pieces;    // results per row, at most
+  bool by_rows;  // no CTA takes chunks of two rows
   size_t max_off, sum_off, key_off, bytes;
 };
 void beam_layout(int num_seqs, int num_beams, int vocab, int select, int dtype, BeamLayout* lay);

@@ -4,8 +4,10 @@
 A score's tolerance: the exponentials of a row are within 26 steps of fp32 (26 2^-23)
 for terms that count (exponents above -20), a thread adds up at most 64 of them in
 fp32 (64 2^-24), the rest is double precision and one rounding to float: 8e-6 +
-2^-24 |score|. Tokens and parents have to be the oracle's, except that candidates
-of different beams whose scores lie closer than that may change places."""
+2^-24 |score|. (Where CTAs walk many chunks a thread adds 17 steps a chunk and one for each
+of at most 16 chunks, 33 2^-24; each move of its reference may add 2 2^-23, and a row of
+random logits moves it a few times.) Tokens and parents have to be the oracle's, except
+that candidates of different beams whose scores lie closer than that may change places."""
 
 import math
 
@@ -199,6 +201,29 @@ def test_one_workspace_for_calls_of_other_sizes():
                        (290, 1, 10, 2), (1, 64, 5000, 16), (3, 2, 100, 5), (200, 1, 64, 4)):
         x, s = make(B, K, V, "bf16", B + V)
         check(run(x, s, n, ws=ws), x, s, n)
+
+
+@pytest.mark.parametrize("dt,B,K,V,n", [
+    ("f16", 80, 4, 50257, 12), ("bf16", 600, 1, 24577, 5), ("f32", 24, 9, 33000, 18),
+    ("bf16", 2, 64, 131080, 64), ("f32", 700, 1, 90, 3), ("f32", 530, 1, 90, 3),
+    ("f16", 150, 4, 8192, 8)])
+def test_shares_that_cross_rows(dt, B, K, V, n):
+    """Enough work for every SM: CTAs walk several chunks, of one row or of several, with rows
+    of ties, masked rows, dead beams and refused ones among them."""
+    x, s = make(B, K, V, dt, B + K + V)
+    x[1::7] = x[1::7].round()
+    x[2::11] = 0.5                             # more ties than a piece ranks at once
+    x[3::13, : V - 40] = -math.inf
+    x[4::17] = -math.inf
+    x[5::19, -1] = math.nan
+    s[::5, 0] = -math.inf
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = pa.beam_workspace(B, K, V, n)
+    out = run(x, s, n, ws=ws, err=err)
+    assert err.item() == pa.PA_DEVERR_LOGITS
+    check(out, x, s, n)
+    for a, b in zip(run(x, s, n, ws=ws), out):
+        assert torch.equal(a, b)
 
 
 def test_refusals_on_device_tensors():
