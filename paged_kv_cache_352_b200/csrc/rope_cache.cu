@@ -15,8 +15,13 @@
 // d/16 lanes of two 8-element chunks: for half-split pairs a lane takes the
 // chunks at 8u and R/2 + 8u, for adjacent pairs 16u and 16u + 8, and in both it
 // needs the table entries 8u .. 8u + 7 of cos and of sin. Those are loaded once
-// per lane and used for every row the lane turns; rows a lane handles are
-// unrolled, their loads issued together.
+// per lane and used for every row the lane turns. What costs time beside the bytes are
+// the chains slot -> place and position -> angles -> row: the first rows are loaded before
+// them, and further rows while the ones before are turned.
+//
+// Measured: 16384 tokens of 32 + 8 heads, d = 128, 16-bit: 67.7 us, 6.1 TB/s (94 % of a
+// copy); 4096 tokens 21.1 us, into E4M3 24.2 us, into 4 bits 23.7 us (the quantization's
+// instructions: 40 % of issue), read back 6.2 us.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -30,14 +35,17 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 
-// Rows of each token that a lane group loads at once, and CTAs per SM: four and five
-// (64 bytes a lane in flight, 96 registers) where rows are copied, two and six where
-// quantizing them needs the registers. 16384 tokens of 32 + 8 heads, 16-bit: 73.0 us
-// with 256 threads and no bound, 71.0 us with two and six, 68.9 us so; 4096 tokens into
-// 4 bits: 27.0, 26.3 and 28.4 us.
+// Rows of each token that a lane group holds at once (as many again are on their way), and
+// CTAs per SM (96 or 80 registers). 4096 tokens of 32 + 8 heads, five and six CTAs: E4M3 24.9
+// and 23.7 us, 4 bits 23.7 and 23.2 us; 16-bit, 16384 tokens: 69.5 and 71.0 us. Four rows
+// loaded at once and none ahead took 27.4, 25.1 and 69.1 us.
 template <typename C>
 struct RopeShape {
-  static constexpr int kUnroll = 4, kCtasPerSm = 5;
+  static constexpr int kUnroll = 2, kCtasPerSm = 5;
+};
+template <>
+struct RopeShape<E4M3> {
+  static constexpr int kUnroll = 2, kCtasPerSm = 6;
 };
 template <>
 struct RopeShape<Int4> {
@@ -100,6 +108,40 @@ __global__ void __launch_bounds__(kRopeThreads, RopeShape<C>::kCtasPerSm)
   const int64_t t = 2 * pair + (sub & 1);
   const bool first_lane = split == 0 && u == 0 && sub < 2;  // of its token, to report
 
+  const bool rot = u < r.rotary_dim / 16;
+  const bool halves = rot && !r.interleaved;
+  // the lane's chunks of a query or key row; of a value row they are 16u, 16u + 8
+  const int off_a = halves ? 8 * u : 16 * u;
+  const int off_b = halves ? r.rotary_dim / 2 + 8 * u : 16 * u + 8;
+  auto fetch = [&](int base, uint4(&raw)[kUnroll][2]) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int row = base + i * RPW + (sub >> 1);
+      raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (row >= row_end || t >= r.num_tokens) continue;
+      const T* src;
+      int oa = off_a, ob = off_b;
+      if (row < r.num_q_heads) {
+        src = static_cast<const T*>(r.q) + t * r.q_stride + (int64_t)row * D;
+      } else {
+        const int h = row - r.num_q_heads;
+        if (h < r.num_kv_heads) {
+          src = static_cast<const T*>(r.key) + t * r.key_stride + (int64_t)h * D;
+        } else {
+          src = static_cast<const T*>(r.value) + t * r.value_stride +
+                (int64_t)(h - r.num_kv_heads) * D;
+          oa = 16 * u;
+          ob = 16 * u + 8;
+        }
+      }
+      raw[i][0] = *reinterpret_cast<const uint4*>(src + oa);
+      raw[i][1] = *reinterpret_cast<const uint4*>(src + ob);
+    }
+  };
+  // the first rows are on their way while slot, position and angles are looked up
+  uint4 raw[kUnroll][2];
+  fetch(row_begin, raw);
+
   bool live = t < r.num_tokens;  // whether anything of this lane's token is written
   const int64_t slot = live ? __ldg(r.slot_mapping + t) : -1;
   bool store = slot >= 0;  // whether its rows are cached
@@ -108,7 +150,6 @@ __global__ void __launch_bounds__(kRopeThreads, RopeShape<C>::kCtasPerSm)
     if (first_lane) report(r.dev_error, PA_DEVERR_SLOT_RANGE);
   }
 
-  const bool rot = u < r.rotary_dim / 16;
   float cs[8], sn[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -146,37 +187,10 @@ __global__ void __launch_bounds__(kRopeThreads, RopeShape<C>::kCtasPerSm)
   const int k_place = tok * (D / 2);
   const int v_place = int4_value_byte<D>(tok, 16 * u);
   const int pair_place = int4_value_byte<D>(tok & ~1, 16 * u + odd8);
-  const bool halves = rot && !r.interleaved;
-  // the lane's chunks of a query or key row; of a value row they are 16u, 16u + 8
-  const int off_a = halves ? 8 * u : 16 * u;
-  const int off_b = halves ? r.rotary_dim / 2 + 8 * u : 16 * u + 8;
 
   for (int base = row_begin; base < row_end; base += RPW * kUnroll) {
-    uint4 raw[kUnroll][2];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int row = base + i * RPW + (sub >> 1);
-      raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (row >= row_end || !live) continue;
-      const T* src;
-      int oa = off_a, ob = off_b;
-      if (row < r.num_q_heads) {
-        src = static_cast<const T*>(r.q) + t * r.q_stride + (int64_t)row * D;
-      } else {
-        if (!store) continue;
-        const int h = row - r.num_q_heads;
-        if (h < r.num_kv_heads) {
-          src = static_cast<const T*>(r.key) + t * r.key_stride + (int64_t)h * D;
-        } else {
-          src = static_cast<const T*>(r.value) + t * r.value_stride +
-                (int64_t)(h - r.num_kv_heads) * D;
-          oa = 16 * u;
-          ob = 16 * u + 8;
-        }
-      }
-      raw[i][0] = *reinterpret_cast<const uint4*>(src + oa);
-      raw[i][1] = *reinterpret_cast<const uint4*>(src + ob);
-    }
+    uint4 next[kUnroll][2];
+    if (base + RPW * kUnroll < row_end) fetch(base + RPW * kUnroll, next);
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int first = base + i * RPW;
@@ -249,6 +263,11 @@ __global__ void __launch_bounds__(kRopeThreads, RopeShape<C>::kCtasPerSm)
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      raw[i][0] = next[i][0];
+      raw[i][1] = next[i][1];
+    }
   }
 }
 
@@ -314,11 +333,13 @@ cudaError_t launch_rope_typed(const RopeArgs& r, cudaStream_t stream) {
   const int rows = r.num_q_heads + 2 * r.num_kv_heads;
   if (r.num_tokens == 0 || rows == 0) return cudaSuccess;
   // Warps that share a token pair's rows: one per RPW rows while the tokens alone do
-  // not give the 148 SMs 64 warps each, fewer as tokens grow (a warp that keeps
-  // a pair's rows loads its cos and sin once).
+  // not give the 148 SMs 32 warps each, fewer as tokens grow (a warp that keeps
+  // a pair's rows looks up its slot, position and angles once). With 64 and 48 instead:
+  // 16384 tokens, 16-bit, 70.1 and 67.7 us against 67.7; 1237 tokens into E4M3 6.0 and 6.0
+  // us against 5.1.
   const int groups = (rows + RPW - 1) / RPW;
   const long long pairs = ((long long)r.num_tokens + 1) / 2;
-  const long long target = 148 * 64;
+  const long long target = 148 * 32;
   long long splits = (target + pairs - 1) / pairs;
   if (splits > groups) splits = groups;
   const int per = (int)((groups + splits - 1) / splits);
