@@ -57,10 +57,10 @@
 // the reference moves; it moves when a weight reaches 2^15, 1/2 of half's range (one
 // test on the packed halves stands for the running maximum of scores and of scales).
 // 7.5 sum w is taken over the rounded weights, so that their errors multiply the
-// centred codes. For half outputs the rounding residual of
-// w joins the product too: with at most 4 query heads per KV head heads repeat
-// in columns 4-7, whose lanes feed the residual (no cost); with 8 it is a second
-// product. For bf16 outputs the weights' 2^-11 is 1/8 of the output's own step.
+// centred codes. What the rounding leaves of w joins the products too, rounded to half
+// again (2^-22 of w in all): with at most 4 query heads per KV head heads repeat in
+// columns 4-7, whose lanes feed it; with 8 it is a second product. Without it the
+// weights' 2^-12 turned about one bf16 output in forty to its neighbour.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -162,8 +162,7 @@ struct Int4State {
   static constexpr int MT = D / 16;
   static constexpr int kCodeBytes = kBlockSize * D / 2;
   static constexpr int kTileBytes = int4_tile_bytes(D);
-  static constexpr bool kResidual = std::is_same<T, __half>::value;
-  static constexpr bool kRepeat = kResidual && G <= 4;  // columns 4-7 repeat heads 0-3
+  static constexpr bool kRepeat = G <= 4;  // columns 4-7 repeat heads 0-3
   static constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
 
   int g, c, lane;
@@ -385,13 +384,11 @@ struct Int4State {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         pb[i] = r.h[b][i];
-        if constexpr (kResidual) {
-          const float2 f = half2_bits_to_float2(r.h[b][i]);
-          const __half2 rl = __floats2half2_rn(r.w[b][i][0] - f.x, r.w[b][i][1] - f.y);
-          memcpy(&lo[i], &rl, 4);
-          if constexpr (kRepeat) pb[i] = c < 2 ? pb[i] : lo[i];
-          else lo[i] = transpose8(lo[i]);
-        }
+        const float2 f = half2_bits_to_float2(r.h[b][i]);
+        const __half2 rl = __floats2half2_rn(r.w[b][i][0] - f.x, r.w[b][i][1] - f.y);
+        memcpy(&lo[i], &rl, 4);
+        if constexpr (kRepeat) pb[i] = c < 2 ? pb[i] : lo[i];
+        else lo[i] = transpose8(lo[i]);
         pb[i] = transpose8(pb[i]);
       }
       const unsigned char* vc = codes + b * 2 * kCodeBytes + kCodeBytes + lane * (4 * W);
@@ -400,14 +397,14 @@ struct Int4State {
       load_words<W>(vc + kCodeBytes / 2, vb);
       constexpr uint32_t kOnes = 0x3c003c00u;
       mma_16816(ow, kOnes, kOnes, kOnes, kOnes, pb[0], pb[1]);
-      if constexpr (kResidual && !kRepeat)
+      if constexpr (!kRepeat)
         mma_16816(ow, kOnes, kOnes, kOnes, kOnes, lo[0], lo[1]);
 #pragma unroll
       for (int q = 0; q < W; ++q) {
         const uint32_t a = va[q], d = vb[q], a8 = a >> 8, d8 = d >> 8;
         mma_16816(o[2 * q], a & kLo, a & kHi, d & kLo, d & kHi, pb[0], pb[1]);
         mma_16816(o[2 * q + 1], a8 & kLo, a8 & kHi, d8 & kLo, d8 & kHi, pb[0], pb[1]);
-        if constexpr (kResidual && !kRepeat) {
+        if constexpr (!kRepeat) {
           mma_16816(o[2 * q], a & kLo, a & kHi, d & kLo, d & kHi, lo[0], lo[1]);
           mma_16816(o[2 * q + 1], a8 & kLo, a8 & kHi, d8 & kLo, d8 & kHi, lo[0], lo[1]);
         }

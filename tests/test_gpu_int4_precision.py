@@ -1,0 +1,97 @@
+"""What the 4-bit decode's weights and sums lose, against the oracle, with a bound that follows
+each token's share of the output.
+
+With p_t the softmax weights, s_t and mid_t the value rows' parameters, P = sum p_t:
+  scores   as in test_gpu_int4: a weight is off by at most e_p = 2 dx + 2^-20 of itself,
+           dx = X 142 2^-23, so an output by 2 e_p sum p_t |v_t| / P
+  weights  w_t = p_t s_t is kept to 2^-20 of itself and to 2^-30 of the largest one
+           (a half and the half of what that rounds off), and acts on centred codes of at most 7.5
+  sums     the matrix instruction's additions round towards zero, by at most 2^-23 of the sum:
+           of the codes' sums, which start again from their centred part every 32 steps of 32
+           tokens (over a window of N tokens at most N / 4 additions, the sums at most 15 w a
+           token and half of that on the way's average), and of the centred sums themselves (at
+           most n / 8 + 64 additions)
+  output   half a step of its type."""
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_352_b200 as pa
+from oracle import int4 as I4
+from oracle.fpbits import bits_to_f64
+from tests.parity import out_to_f64
+from tests.test_gpu_int4 import TDT, Batch, dev16, f32, params
+from workloads import gen
+
+pytestmark = pytest.mark.gpu
+
+WINDOW = 1024
+
+
+def half_step(x, dt):
+    """Half a step of type dt at magnitudes x (and what a rounding just above them takes)."""
+    info = torch.finfo(TDT[dt])
+    e = np.floor(np.log2(np.maximum(np.abs(x) * (1 + 2.0 ** -12), info.tiny)))
+    return info.eps / 2 * 2.0 ** e
+
+
+def rows_of(b, s, h):
+    """(q, k, v, key parameters, value parameters) of one sequence's head in float64."""
+    n = int(b.ctx[s])
+    g = h // (b.hq // b.hkv)
+    blocks = b.tables[s][:-(-n // 16)]
+    kc, vc = (c[torch.from_numpy(blocks).long().cuda()][:, g:g + 1].cpu().numpy()
+              for c in (b.kc, b.vc))
+    cut = lambda x: x[:, 0].reshape(-1, x.shape[-1])[:n]
+    return (bits_to_f64(b.q, b.dt)[s, h], cut(I4.dequantize_cache(kc, False)),
+            cut(I4.dequantize_cache(vc, True)), cut(params(kc)), cut(params(vc)))
+
+
+def bound(b, s, h):
+    """(reference, elementwise bound) of one row."""
+    q, k, v, kp, vp = rows_of(b, s, h)
+    qa, n = np.abs(q).sum(), len(k)
+    X = abs(b.scale) * float(((np.abs(kp[:, 0]) * 15 + np.abs(kp[:, 1])) * qa).max())
+    e_p = 2 * X * 142 * 2.0 ** -23 + 2.0 ** -20
+    z = k @ q * b.scale
+    p = np.exp(z - z.max())
+    P = p.sum()
+    ref = p @ v / P
+    w = p * np.abs(vp[:, 0])
+    centred = p @ np.abs(v - vp[:, 1:]) / P
+    lost = (2 * e_p * (p @ np.abs(v)) / P + 7.5 * (2.0 ** -20 * w.sum() + n * 2.0 ** -30 * w.max()) / P
+            + 2.0 ** -23 * (min(n, WINDOW) / 8 * 15 * w.sum() / P + (n / 8 + 64) * centred))
+    return ref, lost + half_step(np.abs(ref) + lost, b.dt) + 2.0 ** -25
+
+
+def check(b, out, rows=None):
+    got = out_to_f64(out, b.dt)
+    for s in range(len(b.ctx)) if rows is None else rows:
+        for h in range(b.hq):
+            ref, tol = bound(b, s, h)
+            err = np.abs(got[s, h] - ref)
+            assert (err <= tol).all(), (s, h, float(err.max()), float(tol[(err / tol).argmax()]))
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_weights_lose_nothing_that_the_output_keeps(G, d, dt):
+    """Flat scores over value rows of different ranges: an output is within half a step of its
+    type and a hundredth of that."""
+    b = Batch([2, 9, 40, 100, 333], 2 * G, 2, d, dt, 300 + 10 * G + d, qscale=2.0 ** -9)
+    v = f32(b.value, dt) * np.random.default_rng(G).uniform(0.2, 3, b.value.shape[:2])[..., None]
+    write_values(b, v.astype(np.float32))
+    for part in (0, 32):
+        check(b, b.run(part))
+
+
+def write_values(b, v, k=None):
+    b.value = gen.f32_to_bits(v, b.dt)
+    if k is not None:
+        b.key = gen.f32_to_bits(k, b.dt)
+    slots = np.array([int(b.tables[s, p // 16]) * 16 + p % 16
+                      for s in range(len(b.ctx)) for p in range(int(b.ctx[s]))], np.int64)
+    pa.pa_reshape_and_cache_int4(dev16(b.key, b.dt), dev16(b.value, b.dt), b.kc, b.vc,
+                                 torch.from_numpy(slots).cuda())
