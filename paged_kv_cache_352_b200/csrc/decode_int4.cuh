@@ -611,7 +611,9 @@ __global__ void __launch_bounds__(kInt4Warps * 32, kInt4CtasPerSm)
   if (st.g == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      red_m[warp][2 * st.c + e] = st.m[e] == -INFINITY ? -INFINITY : st.ref[e];
+      // no state, or one of NaN scores alone: its NaN has to reach the output, so that its
+      // reference is a number to the merges
+      red_m[warp][2 * st.c + e] = st.m[e] == -INFINITY && st.l[e] == st.l[e] ? -INFINITY : st.ref[e];
       red_l[warp][2 * st.c + e] = st.l[e];
     }
   }
