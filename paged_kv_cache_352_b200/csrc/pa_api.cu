@@ -119,15 +119,20 @@ int default_partition_blocks(int num_seqs, int num_kv_heads, int max_blocks, boo
 // for small batches, which keep one CTA per partition.
 constexpr int kWarpPartMinParts = 16;
 
-bool use_warp_parts(int num_seqs, int num_kv_heads, int part_blocks, int max_parts) {
+// PA_DECODE_SPLIT: 0 (cta), 1 (warp), -1 (the library's choice).
+static int forced_split() {
   static const int forced = [] {
     const char* e = getenv("PA_DECODE_SPLIT");
     if (e && !strcmp(e, "cta")) return 0;
     if (e && !strcmp(e, "warp")) return 1;
     return -1;
   }();
+  return forced;
+}
+
+bool use_warp_parts(int num_seqs, int num_kv_heads, int part_blocks, int max_parts) {
   if (max_parts <= 1) return false;
-  if (forced >= 0) return forced == 1;
+  if (forced_split() >= 0) return forced_split() == 1;
   const long long ctas = (long long)num_kv_heads * num_seqs * ((max_parts + 3) / 4);
   return part_blocks <= kWarpPartMaxBlocks && max_parts >= kWarpPartMinParts &&
          ctas >= kSplitTargetUnits;
@@ -460,7 +465,8 @@ int paged_decode_impl(void* out, const void* q, const void* k_cache, const void*
   a.scale_log2 = scale * 1.4426950408889634f * k_scale;
   a.out_scale = v_scale;
   a.warp_parts = use_warp_parts(num_seqs, num_kv_heads, lay.part_blocks, lay.max_parts);
-  if (small_int4 && !a.warp_parts && units * lay.max_parts >= 2 * kSplitTargetUnits) {
+  if (small_int4 && !a.warp_parts && forced_split() < 0 &&
+      units * lay.max_parts >= 2 * kSplitTargetUnits) {
     // Few sequences of many partitions: a quarter of a partition per warp and a merge
     // launch instead of a merge by each sequence's last CTA (140.0 -> 134.3 us on
     // that batch; 256 sequences of 16-4096 tokens lose by it, 75.6 -> 138.0 us).

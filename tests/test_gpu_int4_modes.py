@@ -1,6 +1,11 @@
 """The 4-bit decode's three ways to merge a split: by each sequence's last CTA, in a second launch
 over warps' partitions, and in a second launch over CTAs' partitions cut into four."""
 
+import os
+import subprocess
+import sys
+
+import numpy as np
 import pytest
 import torch
 
@@ -8,6 +13,33 @@ import paged_kv_cache_352_b200 as pa
 from tests.test_gpu_int4 import Batch, dev16
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+# (sequences, KV heads, longest context, partition): the second launch over CTAs' partitions takes
+# fewer than 1024 (sequence, KV head) pairs that give 2048 partitions and more
+QUARTERED = [(8, 4, 1040, 16), (8, 4, 2100, 32), (8, 4, 3120, 48), (8, 4, 7200, 112),
+             (4, 8, 5200, 80)]
+
+
+def contexts(n, longest, part):
+    """Long, short, empty and ragged ones."""
+    ctx = [longest, 0, 1, part, part + 1, longest - 1, 16 * ((longest - part) // 16), 5 * part - 7]
+    return ctx[:n]
+
+
+@pytest.mark.parametrize("dt,G,d", [("f16", 1, 64), ("bf16", 8, 128), ("f16", 8, 64)])
+@pytest.mark.parametrize("seqs,hkv,longest,part", QUARTERED)
+def test_quartered_partitions(seqs, hkv, longest, part, dt, G, d):
+    ctx = contexts(seqs, longest, part)
+    b = Batch(ctx, G * hkv, hkv, d, dt, part)
+    parts, launches = pa.pa_paged_decode_plan(seqs, G * hkv, hkv, d, b.max_ctx, part)[1:]
+    assert seqs * hkv * parts >= 2048 and launches == 1     # the rule of the 4-bit decode alone
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = b.run(part, err=err)
+    assert err.item() == 0
+    b.check(out)
+    assert torch.equal(out, b.run(part, order=True))
+
 
 # the three modes: (contexts, KV heads, partition)
 MODES = {"last CTA": ([700, 100, 513], 2, 64), "warps": ([1024] * 64, 4, 64),
@@ -51,3 +83,29 @@ def test_nan_rows_show_in_every_mode(mode):
         out = b.run(part)
         assert bool(torch.isnan(out[0, 0]).all())
         assert torch.equal(out[1:], want[1:]) and torch.equal(out[0, 1:], want[0, 1:])
+
+
+FORCED = """
+import sys
+import torch
+import paged_kv_cache_352_b200 as pa
+from tests.test_gpu_int4 import Batch
+b = Batch([1040, 1033, 900, 1040, 17, 1000, 999, 1040], 16, 4, 64, "f16", 8)
+out = b.run(16)
+for s in range(8):
+    one = torch.empty_like(out[s:s + 1])
+    ws = pa.decode_workspace(1, 16, 4, 64, b.max_ctx, 16)
+    pa.pa_paged_decode_int4(one, b.qd[s:s + 1].clone(), b.kc, b.vc, b.t[s:s + 1].clone(),
+                            b.c[s:s + 1].clone(), b.max_ctx, b.scale, 16, ws)
+    assert torch.equal(one[0], out[s]), s
+print("alike")
+"""
+
+
+def test_forced_merge_by_the_last_cta():
+    """PA_DECODE_SPLIT=cta holds for this decode too: a batch gives the bits that its sequences
+    give alone, where nothing else than the merge by the last CTA is chosen."""
+    env = dict(os.environ, PA_DECODE_SPLIT="cta", PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-c", FORCED], capture_output=True, text=True, env=env,
+                       cwd=ROOT, timeout=300)
+    assert r.returncode == 0 and "alike" in r.stdout, r.stdout + r.stderr
