@@ -437,11 +437,17 @@ int pa_beam_select(float* scores, int32_t* parents, int32_t* tokens, const void*
  *                      num_kv_heads < 1024, so that the launch still has ~1024
  *                      (sequence, KV head, partition) units
  *   workspace          device scratch of pa_paged_decode_workspace_size() bytes,
- *                      ZERO-FILLED before its first use; every completed call
- *                      leaves it zero-filled again, so it can be reused without
- *                      clearing. Calls that run concurrently need separate
+ *                      256-byte aligned, ZERO-FILLED before its first use; every
+ *                      completed call leaves zero what the next one needs zero,
+ *                      so that it can be reused without clearing, also for other
+ *                      sizes, heads and cache types: a buffer of the largest size
+ *                      serves all pa_paged_decode, _fp8 and _int4 calls that give
+ *                      the same workspace and workspace_bytes (the buffer's size;
+ *                      another number needs it zeroed again). Other calls' scratch
+ *                      must not be in it. Calls that run concurrently need separate
  *                      workspaces. May be NULL when the size is 0. After a call
- *                      that reported PA_DEVERR_WAIT_TIMEOUT, zero it again.
+ *                      that reported PA_DEVERR_WAIT_TIMEOUT or had a repeated
+ *                      seq_order entry, zero it again.
  *   dev_error          device int or NULL
  * Reduction order depends only on logical token positions, so results are
  * bit-identical whatever the physical placement of blocks and whether blocks

@@ -428,7 +428,8 @@ def pa_paged_decode_cascade_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, 
 
 def decode_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
                      partition_tokens=0, device=None):
-    """A zero-filled workspace tensor of the size pa_paged_decode needs (None if 0)."""
+    """A zero-filled workspace tensor of the size pa_paged_decode needs (None if 0). One of the
+    largest size can be passed, whole, to calls of every size in turn."""
     torch = _torch()
     n = pa_paged_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
                                        max_context_len, BLOCK_SIZE, partition_tokens)

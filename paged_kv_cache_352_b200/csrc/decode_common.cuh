@@ -13,7 +13,8 @@ namespace pa {
 // The split-KV merge in the same launch: called by every thread of a CTA that has
 // stored its partition's state in the workspace. The CTA that completes the
 // sequence's last partition merges all of them in logical order, writes the
-// output rows (times a.out_scale) and returns the counter to zero. `wts`:
+// output rows (times a.out_scale) and returns the counter and the states' maxima and
+// sums to zero. `wts`:
 // >= nparts * G floats of shared memory that no thread reads any more. It ends
 // with a barrier.
 template <typename T, int D, int G, int WARPS>
@@ -38,8 +39,8 @@ __device__ __forceinline__ void merge_if_last(const DecodeArgs& a, float* wts, i
 
   // per-(partition, head) weights exp2(m_p - M) / L, staged in shared memory [nparts][G]
   __shared__ float headM[G], headL[G];
-  const float* pm = a.ws_m + unit * a.max_parts * G;
-  const float* pl = a.ws_l + unit * a.max_parts * G;
+  float* pm = a.ws_m + unit * a.max_parts * G;
+  float* pl = a.ws_l + unit * a.max_parts * G;
   for (int g = warp; g < G; g += WARPS) {
     float M = -INFINITY;
     for (int p = lane; p < nparts; p += 32) M = fmaxf(M, __ldcg(pm + p * G + g));
@@ -117,6 +118,8 @@ __device__ __forceinline__ void merge_if_last(const DecodeArgs& a, float* wts, i
     memcpy(&packed, r, sizeof(packed));
     *reinterpret_cast<uint2*>(out_rows + 4 * it) = packed;
   }
+  // leave zeros: in a call of another size, merge counters may lie here
+  for (int idx = threadIdx.x; idx < nparts * G; idx += blockDim.x) pm[idx] = pl[idx] = 0.f;
   if (threadIdx.x == 0) a.ws_count[unit] = 0;
   __syncthreads();
 }

@@ -92,6 +92,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_partitions_kernel(const D
     set_l[set] = L;
   }
   __syncthreads();
+  // leave zeros: in a call of another size, merge counters may lie here
+  for (int p = tid; p < nparts; p += kMergeThreads)
+    a.ws_m[base + (size_t)p * G] = a.ws_l[base + (size_t)p * G] = 0.f;
   if (set != 0) return;
   float Mt = -INFINITY;
 #pragma unroll

@@ -452,7 +452,16 @@ int paged_decode_impl(void* out, const void* q, const void* k_cache, const void*
   a.ws_count = lay.bytes ? reinterpret_cast<int*>(ws + lay.count_off) : nullptr;
   a.ws_m = lay.bytes ? reinterpret_cast<float*>(ws + lay.ml_off) : nullptr;
   a.ws_l = lay.bytes ? a.ws_m + (size_t)num_seqs * num_kv_heads * lay.max_parts * group : nullptr;
-  a.ws_acc = lay.bytes ? reinterpret_cast<float*>(ws + lay.acc_off) : nullptr;
+  // A merge relies on counters that are zero before it, in a buffer W = workspace_bytes that
+  // calls of other sizes wrote to. Of U (sequence, KV head) pairs in a split, the 4 U bytes of
+  // counters lie in the buffer's first W / 133, since such a call needs 532 U bytes and more
+  // (two partitions of one head of 64 elements). The merges return counters, maxima and sums
+  // to zero; the accumulators, which they leave as they are, go to the buffer's end: they start
+  // behind maxima and sums, at W / 65 - 510 and 512 bytes or later (64 of 65 bytes of a state
+  // at most are its accumulators), so that no call's counters reach into them.
+  a.ws_acc = lay.bytes ? reinterpret_cast<float*>(
+                             ws + lay.acc_off + ((workspace_bytes - lay.bytes) & ~size_t(255)))
+                       : nullptr;
   a.dev_error = dev_error;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.max_context_len = max_context_len;
