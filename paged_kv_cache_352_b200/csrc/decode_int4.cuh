@@ -52,10 +52,12 @@
 // heads 2c, 2c + 1 again. One more product with ones for V gives sum w.
 //
 // Precision. Products are exact, sums are fp32. q is brought below 2^15 by a
-// power of two (exact in half unless 2^29 below the row's largest element). The
-// weights w are rounded to half precision in units that put the largest at 2^7 when
+// power of two (exact in half unless 2^28 below the row's largest element, or 2^24 at the
+// dimensions of high nibbles, whose operand is q / 16: 2^-35 of that element is lost). The
+// weights w are rounded to half precision in units that put the largest at 2^6 to 2^7 when
 // the reference moves; it moves when a weight reaches 2^15, 1/2 of half's range (one
-// test on the packed halves stands for the running maximum of scores and of scales).
+// test on the packed halves), and follows the largest w = p s, not p and s apart: behind
+// constant rows (s = 0) of high scores, or beside a large row of none, weights keep their bits.
 // 7.5 sum w is taken over the rounded weights, so that their errors multiply the
 // centred codes. What the rounding leaves of w joins the products too, rounded to half
 // again (2^-22 of w in all): with at most 4 query heads per KV head heads repeat in
@@ -168,13 +170,10 @@ struct Int4State {
   int g, c, lane;
   uint4 qraw[W];
   uint32_t qb[KSTEPS][2];           // head g's operand
-  // Of heads 2c, 2c + 1. Everything accumulated is in units of 2^ref: ref is the
-  // softmax reference m plus log2 S - 7, S a power of two at or above the largest
-  // value scale when the reference last moved (0 before a positive one). l and pmid
-  // are this lane's share (tokens g, g + 8).
-  float m[2], ref[2], l[2], pmid[2], row_scale[2], qsum[2];
+  // Of heads 2c, 2c + 1. Everything accumulated is in units of 2^ref (-inf before the
+  // first step). l and pmid are this lane's share (tokens g, g + 8).
+  float ref[2], l[2], pmid[2], row_scale[2], qsum[2];
   float centre[4];  // -7.5 qsum, where the products of a tile start
-  float vmax;       // S
   float o[MT][4], ow[4];
 
   // the head of column h
@@ -228,10 +227,9 @@ struct Int4State {
       qsum[e] = qs[e];
       row_scale[e] = __shfl_sync(0xffffffffu, rs, 8 * c + 4 * e);
       centre[e] = centre[2 + e] = -7.5f * qsum[e];
-      m[e] = ref[e] = -INFINITY;
+      ref[e] = -INFINITY;
       l[e] = pmid[e] = 0.f;
     }
-    vmax = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       ow[e] = 0.f;
@@ -252,7 +250,7 @@ struct Int4State {
     float w[2][2][2];   // [block][i][e]
     uint32_t h[2][2];   // the same as halves
     // Whether a weight leaves the range: some w at or past 2^15 (or inf or NaN, which a
-    // reference of -inf gives too), or p far past what S = its scale would allow.
+    // reference of -inf gives too), or p past 2^60 (the reference leaves 2^31 at most).
     __device__ __forceinline__ bool out_of_range() const {
       const uint32_t m = __vmaxu2(__vmaxu2(h[0][0], h[0][1]), __vmaxu2(h[1][0], h[1][1]));
       return ((m + 0x08000800u) & 0x80008000u) != 0u || !(p[0] + p[1] <= 1.15e18f);
@@ -284,37 +282,34 @@ struct Int4State {
 
   // Moves the references to cover a step whose weights left the range (the first step
   // among them), and brings what has accumulated to the new ones, which are the same in
-  // every lane of a column. After it no weight of the step is past 2^7.
+  // every lane of a column. A token's weight counts with its own scale, so that the largest
+  // w of the step is put at 2^6 to 2^7 whatever the other tokens' scales are, a constant
+  // row's (0) as the smallest half: p is 2^31 at most.
   template <bool kMask>
   __device__ __forceinline__ void move(const float (&t)[2][4], const float2 (&vp)[2][2],
                                        int valid0, int valid1) {
     float bmax[2] = {-INFINITY, -INFINITY};
-    float smax = 0.f;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        smax = fmaxf(smax, vp[b][i].x);
+      for (int i = 0; i < 2; ++i)
         if (!kMask || g + 8 * i < (b ? valid1 : valid0)) {
-          bmax[0] = fmaxf(bmax[0], t[b][2 * i] * row_scale[0]);
-          bmax[1] = fmaxf(bmax[1], t[b][2 * i + 1] * row_scale[1]);
+          // log2 of the power of two at or above the scale (exact: a half has 11 bits)
+          const uint32_t s = __float_as_uint(fmaxf(vp[b][i].x, 5.9604644775390625e-8f));
+          const float up = (float)((int)((s + 0x007fffffu) >> 23) - 127);
+          bmax[0] = fmaxf(bmax[0], fmaf(t[b][2 * i], row_scale[0], up));
+          bmax[1] = fmaxf(bmax[1], fmaf(t[b][2 * i + 1], row_scale[1], up));
         }
-      }
 #pragma unroll
     for (int mask = 4; mask <= 16; mask <<= 1) {
       bmax[0] = fmaxf(bmax[0], __shfl_xor_sync(0xffffffffu, bmax[0], mask));
       bmax[1] = fmaxf(bmax[1], __shfl_xor_sync(0xffffffffu, bmax[1], mask));
-      smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, mask));
     }
-    // S: the power of two at or above every scale looked at (a half: exact here)
-    if (smax > vmax)
-      vmax = __uint_as_float((__float_as_uint(smax) + 0x007fffffu) & 0x7f800000u);
-    const float shift = vmax > 0.f ? (float)((int)(__float_as_uint(vmax) >> 23) - 127 - 7) : 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const bool first = m[e] == -INFINITY;  // nothing of this head has accumulated
-      m[e] = fmaxf(m[e], bmax[e]);
-      const float to = (m[e] == -INFINITY ? 0.f : m[e]) + shift;
+      const bool first = ref[e] == -INFINITY;  // nothing of this head has accumulated
+      // (scores of NaN or -inf alone leave a first reference at 0, a number to the merges)
+      const float to = bmax[e] == -INFINITY ? (first ? 0.f : ref[e]) : fmaxf(ref[e], bmax[e] - 7.f);
       const float alpha = first ? 1.f : fast_exp2(ref[e] - to);
       ref[e] = to;
       l[e] *= alpha;
@@ -611,9 +606,7 @@ __global__ void __launch_bounds__(kInt4Warps * 32, kInt4CtasPerSm)
   if (st.g == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      // no state, or one of NaN scores alone: its NaN has to reach the output, so that its
-      // reference is a number to the merges
-      red_m[warp][2 * st.c + e] = st.m[e] == -INFINITY && st.l[e] == st.l[e] ? -INFINITY : st.ref[e];
+      red_m[warp][2 * st.c + e] = st.ref[e];
       red_l[warp][2 * st.c + e] = st.l[e];
     }
   }

@@ -95,3 +95,69 @@ def write_values(b, v, k=None):
                       for s in range(len(b.ctx)) for p in range(int(b.ctx[s]))], np.int64)
     pa.pa_reshape_and_cache_int4(dev16(b.key, b.dt), dev16(b.value, b.dt), b.kc, b.vc,
                                  torch.from_numpy(slots).cuda())
+
+
+def directed(b, offsets):
+    """Keys that give sequence 0's tokens the scores `offsets` (head 0's KV head; q one-hot)."""
+    q = np.zeros((1, b.hq, b.d), np.float32)
+    q[:, :, 0] = 8.0
+    b.q = gen.f32_to_bits(q, b.dt)
+    b.qd = dev16(b.q, b.dt)
+    k = np.zeros((len(offsets), b.hkv, b.d), np.float32)
+    k[:, :, 0] = (np.asarray(offsets) / (8.0 * b.scale))[:, None]
+    return k
+
+
+@pytest.mark.parametrize("G", [1, 8])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("lead", [32, 500])
+def test_small_values_behind_constant_rows(dt, G, lead):
+    """Tokens of high scores and constant value rows (scale 0), then thousands of low scores and
+    small values: what the latter add is all there is, and no weight of theirs may underflow."""
+    n = 3000
+    b = Batch([n], G, 1, 64, dt, 51)
+    off = np.where(np.arange(n) < lead, 0.0, -8.0)
+    k = directed(b, off)
+    v = f32(b.value, dt) * np.float32(2.0 ** -3 if dt == "f16" else 2.0 ** -9)
+    v[:lead] = 0.0
+    write_values(b, v, k)
+    for part in (0, 4096, 128):
+        out = b.run(part)
+        check(b, out)
+        assert out.abs().max() > 0
+
+
+@pytest.mark.parametrize("G", [1, 8])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_small_values_beside_a_large_row_of_no_weight(dt, G):
+    """A value row of thousands whose softmax weight is e^-40, first or last, beside rows a
+    millionth as large and smaller: the large row's scale must not cost the small ones their weights' bits."""
+    for place in (0, 40, 89):
+        b = Batch([90], G, 1, 128, dt, 52)
+        off = np.zeros(90)
+        off[place] = -40.0
+        k = directed(b, off)
+        small, ratio = (-8, 22) if dt == "f16" else (-13, 28)
+        v = f32(b.value, dt) * np.float32(2.0 ** small)
+        v[place] *= np.float32(2.0 ** ratio)
+        write_values(b, v, k)
+        for part in (0, 32):
+            check(b, b.run(part))
+
+
+def test_references_at_both_ends():
+    """Constant rows alone, constant rows of far higher scores after others, scores that rise by
+    hundreds, and the smallest scale a row can have."""
+    b = Batch([256], 2, 1, 64, "bf16", 53)
+    for off, rows in ((np.zeros(256), slice(0, 256)), (np.arange(256) * 3.0, slice(64, 128)),
+                      (np.arange(256) * -3.0, slice(0, 64)),
+                      (np.where(np.arange(256) < 128, 0.0, 300.0), slice(128, 256))):
+        k = directed(b, off)
+        v = f32(b.value, "bf16").copy()
+        v[rows] = 0.5
+        write_values(b, v, k)
+        check(b, b.run())
+        v[:] = 2.0 ** -24 * np.random.default_rng(1).integers(-7, 9, v.shape)
+        write_values(b, v, k)
+        assert params(b.vc.cpu().numpy())[b.tables[0], 0, :, 0].max() <= 2.0 ** -23
+        check(b, b.run())
