@@ -61,8 +61,11 @@
 // 7.5 sum w is taken over the rounded weights, so that their errors multiply the
 // centred codes. What the rounding leaves of w joins the products too, rounded to half
 // again (2^-22 of w in all): with at most 4 query heads per KV head heads repeat in
-// columns 4-7, whose lanes feed it; with 8 it is a second product. Without it the
-// weights' 2^-12 turned about one bf16 output in forty to its neighbour.
+// columns 4-7, whose lanes feed it, with 8 it is a second product for half outputs.
+// For bf16 outputs of 8 heads w stays at its 2^-12, a sixteenth of half the output's step:
+// the second product took 8 long sequences from 154 to 173 us and brought the outputs'
+// relative difference from 32-bit sums from 1.0e-3 to 0.8e-3; with 4 heads,
+// where it costs 3 %, from 8e-4 to 2e-4.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -165,6 +168,7 @@ struct Int4State {
   static constexpr int kCodeBytes = kBlockSize * D / 2;
   static constexpr int kTileBytes = int4_tile_bytes(D);
   static constexpr bool kRepeat = G <= 4;  // columns 4-7 repeat heads 0-3
+  static constexpr bool kSecond = G == 8 && std::is_same<T, __half>::value;  // residuals' own
   static constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
 
   int g, c, lane;
@@ -383,7 +387,7 @@ struct Int4State {
         const __half2 rl = __floats2half2_rn(r.w[b][i][0] - f.x, r.w[b][i][1] - f.y);
         memcpy(&lo[i], &rl, 4);
         if constexpr (kRepeat) pb[i] = c < 2 ? pb[i] : lo[i];
-        else lo[i] = transpose8(lo[i]);
+        else if constexpr (kSecond) lo[i] = transpose8(lo[i]);
         pb[i] = transpose8(pb[i]);
       }
       const unsigned char* vc = codes + b * 2 * kCodeBytes + kCodeBytes + lane * (4 * W);
@@ -392,14 +396,14 @@ struct Int4State {
       load_words<W>(vc + kCodeBytes / 2, vb);
       constexpr uint32_t kOnes = 0x3c003c00u;
       mma_16816(ow, kOnes, kOnes, kOnes, kOnes, pb[0], pb[1]);
-      if constexpr (!kRepeat)
+      if constexpr (kSecond)
         mma_16816(ow, kOnes, kOnes, kOnes, kOnes, lo[0], lo[1]);
 #pragma unroll
       for (int q = 0; q < W; ++q) {
         const uint32_t a = va[q], d = vb[q], a8 = a >> 8, d8 = d >> 8;
         mma_16816(o[2 * q], a & kLo, a & kHi, d & kLo, d & kHi, pb[0], pb[1]);
         mma_16816(o[2 * q + 1], a8 & kLo, a8 & kHi, d8 & kLo, d8 & kHi, pb[0], pb[1]);
-        if constexpr (!kRepeat) {
+        if constexpr (kSecond) {
           mma_16816(o[2 * q], a & kLo, a & kHi, d & kLo, d & kHi, lo[0], lo[1]);
           mma_16816(o[2 * q + 1], a8 & kLo, a8 & kHi, d8 & kLo, d8 & kHi, lo[0], lo[1]);
         }
