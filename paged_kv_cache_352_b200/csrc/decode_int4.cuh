@@ -18,13 +18,13 @@
 //     17 a tile). The contraction has G columns of work, far too few for tcgen05;
 //   - codes are operands as they lie: the low four bits of a half with zero
 //     exponent are worth n 2^-24, the next four n 2^-20, both exact. Of a word of
-//     eight codes, w & 0x000f000f and w & 0x00f000f0 are operand registers, and
-//     the same masks of w >> 8 give the rest: 5 instructions for 8 codes. The
-//     powers of two are taken back in the query operand (1/16 at the dimensions
-//     of high nibbles) and in the fp32 results. (Value codes could do with 4, whole
-//     bytes and high nibbles whose sums are subtracted at the end; but the bytes' sums are
-//     16 times as large and a long context's mean is what is left of them: the error
-//     over 32k-131k tokens grew from 0.17% to 0.52%);
+//     eight key codes, w & 0x000f000f and w & 0x00f000f0 are operand registers, and
+//     the same masks of w >> 8 give the rest: 5 instructions for 8 codes; value codes
+//     take two bits more (w << 2 and w >> 6), see Precision. The powers of two are taken
+//     back in the query operand (1/16 at the dimensions of high nibbles) and in the fp32
+//     results. (Value codes could do with 4, whole bytes and high nibbles whose sums are
+//     subtracted at the end; but the bytes' sums are 16 times as large and a long context's
+//     mean is what is left of them: the error over 32k-131k tokens grew from 0.17% to 0.52%);
 //   - the cache layout (int4_cache.cuh) gives each lane the 16 bytes it feeds to
 //     its own registers, so lanes copy their own chunks by cp.async: no barrier,
 //     no lane that issues for the others, 9 copies per two blocks;
@@ -51,7 +51,15 @@
 // shifted, dimensions +2 and +3 for the next m-tile. The result's columns are
 // heads 2c, 2c + 1 again. One more product with ones for V gives sum w.
 //
-// Precision. Products are exact, sums are fp32. q is brought below 2^15 by a
+// Precision. Products are exact, sums are fp32. The matrix instruction, though, cuts its
+// addends (towards zero) at about 2^-24 of the largest, and takes a subnormal code's size from
+// its exponent field: n 2^-24 counts as 2^-14. What a token loses is of one sign for all
+// dimensions. So value codes are shifted to 2^-22 and 2^-18 (one shift more per word), a step's
+// products start from -7.5 sum w and end near 0, and they join the running sums by ordinary fp32
+// additions, rounded to nearest. With running sums as the accumulator and codes at 2^-24 and
+// 2^-20, half outputs over 131072 tokens of normal scores were off by 2.4e-4 of their norm
+// beside their rounding's 2.1e-4; now by 7e-6 (scores twice as wide: 5.7e-4, 7e-5). It costs
+// 3.5 % (one head per KV head), 3.5 % (4) and 4 % (8). q is brought below 2^15 by a
 // power of two (exact in half unless 2^28 below the row's largest element, or 2^24 at the
 // dimensions of high nibbles, whose operand is q / 16: 2^-35 of that element is lost). The
 // weights w are rounded to half precision in units that put the largest at 2^6 to 2^7 when
@@ -87,7 +95,6 @@ namespace {
 constexpr int kInt4Warps = 4;
 constexpr int kInt4Stages = 3;
 constexpr int kInt4CtasPerSm = 4;  // 128 registers a thread
-constexpr int kRecentre = 32;      // steps between recentrings of the output sums
 
 // A lane's four chunks of a block's codes: two of K, two of V.
 template <int CB>
@@ -178,7 +185,7 @@ struct Int4State {
   // first step). l and pmid are this lane's share (tokens g, g + 8).
   float ref[2], l[2], pmid[2], row_scale[2], qsum[2];
   float centre[4];  // -7.5 qsum, where the products of a tile start
-  float o[MT][4], ow[4];
+  float o[MT][4];   // sum w (n - 7.5), in the products' units
 
   // the head of column h
   static __device__ __forceinline__ int head(int h) { return kRepeat ? (h & 3) : h; }
@@ -235,11 +242,9 @@ struct Int4State {
       l[e] = pmid[e] = 0.f;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      ow[e] = 0.f;
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
       for (int t = 0; t < MT; ++t) o[t][e] = 0.f;
-    }
   }
 
   // (scale, mid) of token t
@@ -323,7 +328,6 @@ struct Int4State {
         o[i][e] *= alpha;
         o[i][2 + e] *= alpha;
       }
-      ow[e] *= alpha;
     }
   }
 
@@ -376,56 +380,59 @@ struct Int4State {
       l[e] += r.p[e];
       pmid[e] += r.pm[e];
     }
-    // ---- O^T += V^T P^T
+    // ---- O^T += V^T P^T - 7.5 sum w
+    uint32_t pb[2][2], lo[2][2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint32_t pb[2], lo[2];
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        pb[i] = r.h[b][i];
         const float2 f = half2_bits_to_float2(r.h[b][i]);
         const __half2 rl = __floats2half2_rn(r.w[b][i][0] - f.x, r.w[b][i][1] - f.y);
-        memcpy(&lo[i], &rl, 4);
-        if constexpr (kRepeat) pb[i] = c < 2 ? pb[i] : lo[i];
-        else if constexpr (kSecond) lo[i] = transpose8(lo[i]);
-        pb[i] = transpose8(pb[i]);
+        memcpy(&lo[b][i], &rl, 4);
+        pb[b][i] = r.h[b][i];
+        if constexpr (kRepeat) pb[b][i] = c < 2 ? pb[b][i] : lo[b][i];
+        else if constexpr (kSecond) lo[b][i] = transpose8(lo[b][i]);
+        pb[b][i] = transpose8(pb[b][i]);
       }
-      const unsigned char* vc = codes + b * 2 * kCodeBytes + kCodeBytes + lane * (4 * W);
-      uint32_t va[W], vb[W];
-      load_words<W>(vc, va);
-      load_words<W>(vc + kCodeBytes / 2, vb);
-      constexpr uint32_t kOnes = 0x3c003c00u;
-      mma_16816(ow, kOnes, kOnes, kOnes, kOnes, pb[0], pb[1]);
-      if constexpr (kSecond)
-        mma_16816(ow, kOnes, kOnes, kOnes, kOnes, lo[0], lo[1]);
-#pragma unroll
-      for (int q = 0; q < W; ++q) {
-        const uint32_t a = va[q], d = vb[q], a8 = a >> 8, d8 = d >> 8;
-        mma_16816(o[2 * q], a & kLo, a & kHi, d & kLo, d & kHi, pb[0], pb[1]);
-        mma_16816(o[2 * q + 1], a8 & kLo, a8 & kHi, d8 & kLo, d8 & kHi, pb[0], pb[1]);
-        if constexpr (kSecond) {
-          mma_16816(o[2 * q], a & kLo, a & kHi, d & kLo, d & kHi, lo[0], lo[1]);
-          mma_16816(o[2 * q + 1], a8 & kLo, a8 & kHi, d8 & kLo, d8 & kHi, lo[0], lo[1]);
-        }
-      }
+    constexpr uint32_t kOnes = 0x3c003c00u;
+    float sw[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_16816(sw, kOnes, kOnes, kOnes, kOnes, pb[0][0], pb[0][1]);
+    mma_16816(sw, kOnes, kOnes, kOnes, kOnes, pb[1][0], pb[1][1]);
+    if constexpr (kSecond) {
+      float sl[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_16816(sl, kOnes, kOnes, kOnes, kOnes, lo[0][0], lo[0][1]);
+      mma_16816(sl, kOnes, kOnes, kOnes, kOnes, lo[1][0], lo[1][1]);
+      sw[0] += sl[0];
+      sw[1] += sl[1];
     }
-  }
-
-  // Takes 7.5 sum w out of the output sums so far. The matrix instruction's additions
-  // round towards zero, which costs half a step of the sum each: over codes of mean 7.5 the
-  // sums grow with the context while their centred part does not. Every kRecentre steps
-  // the sums start again from the centred part (an error of 2^-24 7.5 kRecentre of the
-  // weights' scale, whatever the length).
-  __device__ __forceinline__ void recentre() {
+    // -7.5 sum w in the products' units (2^-22 at low nibbles, 2^-18 at high ones)
+    const float start[4] = {sw[0] * -1.7881393432617188e-06f, sw[1] * -1.7881393432617188e-06f,
+                            sw[0] * -2.86102294921875e-05f, sw[1] * -2.86102294921875e-05f};
+    uint32_t va[2][W], vb[2][W];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float w = -7.5f * ow[e];
+    for (int b = 0; b < 2; ++b) {
+      const unsigned char* vc = codes + b * 2 * kCodeBytes + kCodeBytes + lane * (4 * W);
+      load_words<W>(vc, va[b]);
+      load_words<W>(vc + kCodeBytes / 2, vb[b]);
+    }
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        o[i][e] = fmaf(w, 5.9604644775390625e-8f, o[i][e]);           // 2^-24
-        o[i][2 + e] = fmaf(w, 9.5367431640625e-7f, o[i][2 + e]);      // 2^-20
+    for (int t = 0; t < MT; ++t) {
+      float d[4];
+      uint32_t a[2][4];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t x = t & 1 ? va[b][t >> 1] >> 6 : va[b][t >> 1] << 2;
+        const uint32_t y = t & 1 ? vb[b][t >> 1] >> 6 : vb[b][t >> 1] << 2;
+        a[b][0] = x & 4 * kLo, a[b][1] = x & 4 * kHi, a[b][2] = y & 4 * kLo, a[b][3] = y & 4 * kHi;
       }
-      ow[e] = 0.f;
+      mma_16816_from(d, start, a[0][0], a[0][1], a[0][2], a[0][3], pb[0][0], pb[0][1]);
+      mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], pb[1][0], pb[1][1]);
+      if constexpr (kSecond) {  // behind the weights, whose sum is near 0 by now
+        mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], lo[0][0], lo[0][1]);
+        mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], lo[1][0], lo[1][1]);
+      }
+      fadd2(o[t][0], o[t][1], d[0], d[1]);
+      fadd2(o[t][2], o[t][3], d[2], d[3]);
     }
   }
 
@@ -447,11 +454,10 @@ struct Int4State {
   // Unnormalised outputs (in units of 2^ref) of head 2c + e: dimensions
   // 4W g + 4q .. + 3.
   __device__ __forceinline__ float4 row4(int e, int q) const {
-    const float base = fmaf(-7.5f, ow[e], pmid[e]);
-    return make_float4(fmaf(o[2 * q][e], 16777216.f, base),
-                       fmaf(o[2 * q][2 + e], 1048576.f, base),
-                       fmaf(o[2 * q + 1][e], 16777216.f, base),
-                       fmaf(o[2 * q + 1][2 + e], 1048576.f, base));
+    return make_float4(fmaf(o[2 * q][e], 4194304.f, pmid[e]),
+                       fmaf(o[2 * q][2 + e], 262144.f, pmid[e]),
+                       fmaf(o[2 * q + 1][e], 4194304.f, pmid[e]),
+                       fmaf(o[2 * q + 1][2 + e], 262144.f, pmid[e]));
   }
 };
 
@@ -598,7 +604,6 @@ __global__ void __launch_bounds__(kInt4Warps * 32, kInt4CtasPerSm)
       st.template step<true>(codes, codes + Stage::kParOff, (miss & 1u) ? 0 : v0,
                              (miss & 2u) ? 0 : v0 - kBlockSize);
     stg = stg == STAGES - 1 ? 0 : stg + 1;
-    if ((j & (kRecentre - 1)) == kRecentre - 1) st.recentre();
   }
   cp_async_wait<0>();
 

@@ -7,11 +7,12 @@ With p_t the softmax weights, s_t and mid_t the value rows' parameters, P = sum 
   weights  w_t = p_t s_t is kept to 2^-20 of itself and to 2^-30 of the largest one
            (a half and the half of what that rounds off; for bf16 outputs of 8 query heads per
            KV head the first alone, 2^-11), and acts on centred codes of at most 7.5
-  sums     the matrix instruction's additions round towards zero, by at most 2^-23 of the sum:
-           of the codes' sums, which start again from their centred part every 32 steps of 32
-           tokens (over a window of N tokens at most N / 4 additions, the sums at most 15 w a
-           token and half of that on the way's average), and of the centred sums themselves (at
-           most n / 8 + 64 additions)
+  sums     of a step (two blocks) the matrix instruction cuts its addends at 2^-23 of the largest,
+           a code's operand counting as 2^9 of it, so at 2^-14 of the step's largest w: the running
+           sum in each of at most 8 products, and of the weights' products those of an eighth of
+           the largest and less (others end above that: 11 bits), at most 4 a token. The sum that
+           the codes are centred by: 34 additions at 2^-23 of it, times 7.5. Steps add up in fp32,
+           rounded to nearest: n / 128 + 64 additions a warp at 2^-24 of the centred sums
   output   half a step of its type."""
 
 import numpy as np
@@ -26,8 +27,6 @@ from tests.test_gpu_int4 import TDT, Batch, dev16, f32, params
 from workloads import gen
 
 pytestmark = pytest.mark.gpu
-
-WINDOW = 1024
 
 
 def half_step(x, dt):
@@ -49,6 +48,16 @@ def rows_of(b, s, h):
             cut(I4.dequantize_cache(vc, True)), cut(params(kc)), cut(params(vc)))
 
 
+def cut_in_steps(w):
+    """What the steps' products may lose, in codes times weights. A step is at most a block and a
+    neighbour of it, however the blocks pair up."""
+    blocks = np.pad(w, (0, -len(w) % 16)).reshape(-1, 16)
+    m = np.pad(blocks.max(1), 1)
+    m = np.maximum(np.maximum(m[:-2], m[1:-1]), m[2:])
+    small = ((blocks > 0) & (blocks < m[:, None] / 8)).sum(1)
+    return 2.0 ** -14 * float((m * (4 + 4 * small)).sum())
+
+
 def bound(b, s, h):
     """(reference, elementwise bound) of one row."""
     q, k, v, kp, vp = rows_of(b, s, h)
@@ -63,7 +72,8 @@ def bound(b, s, h):
     centred = p @ np.abs(v - vp[:, 1:]) / P
     e_w = 2.0 ** -11 if b.dt == "bf16" and b.hq == 8 * b.hkv else 2.0 ** -20
     lost = (2 * e_p * (p @ np.abs(v)) / P + 7.5 * (e_w * w.sum() + n * 2.0 ** -30 * w.max()) / P
-            + 2.0 ** -23 * (min(n, WINDOW) / 8 * 15 * w.sum() / P + (n / 8 + 64) * centred))
+            + (cut_in_steps(w) + 255 * 2.0 ** -23 * w.sum()) / P
+            + (n / 128 + 64) * 2.0 ** -24 * centred)
     return ref, lost + half_step(np.abs(ref) + lost, b.dt) + 2.0 ** -25
 
 
@@ -163,3 +173,38 @@ def test_references_at_both_ends():
         write_values(b, v, k)
         assert params(b.vc.cpu().numpy())[b.tables[0], 0, :, 0].max() <= 2.0 ** -23
         check(b, b.run())
+
+
+@pytest.mark.parametrize("dt,G", [("f16", 1), ("f16", 8), ("bf16", 4)])
+@pytest.mark.parametrize("part", [65536, 8192, 0])
+def test_long_tail_beside_large_rows(dt, G, part):
+    """65536 tokens of equal weights: a row thousands of times as large as the others at the front,
+    its negative at the end, and what is left, a mean of all the small ones, must not be cut at
+    the large row's size all the way."""
+    n = 65536
+    b = Batch([n], G, 1, 128, dt, 54)
+    b.q = np.zeros_like(b.q)
+    b.qd = dev16(b.q, dt)
+    v = f32(b.value, dt) * np.float32(0.25)
+    v[:32] = v[-32:] = 0.0                      # no others in the large rows' steps
+    v[0] = np.random.default_rng(2).uniform(-4000, 4000, 128)
+    v[-1] = -v[0]
+    write_values(b, v)
+    check(b, b.run(part))
+
+
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_means_are_as_good_as_half(G):
+    """131072 tokens with scores of unit variance: the outputs, a 140th of a value, take no more
+    error from weights and sums than a quarter of half precision's half step, beside the rounding
+    itself (which the reference tells exactly). Sums of 32 bits rounded to nearest leave 2^-21."""
+    b = Batch([131072], G, 1, 128, "f16", 43)
+    got = out_to_f64(b.run(2048)[0], "f16")
+    err, rounding, norm = 0.0, 0.0, 0.0
+    for h in range(G):
+        q, k, v, _, _ = rows_of(b, 0, h)
+        ref = I4.softmax_attention(q, k, v, b.scale)
+        err += ((got[h] - ref) ** 2).sum()
+        rounding += ((ref.astype(np.float16) - ref) ** 2).sum()
+        norm += (ref ** 2).sum()
+    assert err <= rounding + 2.0 ** -26 * norm, ((err / norm) ** 0.5, (rounding / norm) ** 0.5)
