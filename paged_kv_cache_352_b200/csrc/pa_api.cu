@@ -1214,6 +1214,7 @@ int pa_beam_select(float* scores, int32_t* parents, int32_t* tokens, const void*
   a.num_beams = num_beams;
   a.vocab = vocab;
   a.select = num_select;
+  a.dtype = dtype;
   a.workspace = workspace;
   a.dev_error = dev_error;
   return cuda_status(launch_beam_select(a, dtype, static_cast<cudaStream_t>(stream)),

@@ -192,7 +192,7 @@ struct BeamArgs {
   const void* logits;
   int64_t row_stride;
   const float* beam_scores;
-  int num_seqs, num_beams, vocab, select;
+  int num_seqs, num_beams, vocab, select, dtype;
   void* workspace;
   int* dev_error;
 };
