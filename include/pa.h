@@ -373,7 +373,9 @@ int pa_rope_table(float* cos_sin, int num_positions, int rotary_dim, double thet
  * of -inf is no candidate: a beam score of -inf (an ended beam, or all but one
  * before the first step) or a logit of -inf (a masked token) takes it out. A beam
  * with a NaN or +inf among its logits, or as its score, gives no candidates
- * (PA_DEVERR_LOGITS). Places left over get score -inf, parent -1, token -1.
+ * (PA_DEVERR_LOGITS). Places left over get score -inf, parent -1, token -1; a
+ * candidate whose score is below the lowest float (a beam score and a masked
+ * logit both near it) gets that.
  *
  *   scores, parents, tokens   device, float / int32 / int32 [num_seqs][num_select]
  *   logits        device, [num_seqs * num_beams][vocab] of type dtype (PA_F16,

@@ -37,6 +37,7 @@
 // of each other tie. It takes a row of 131072 logits again in 31 us; of 3840 sequences of
 // random logits (8 beams, 16 places) none needed it.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
@@ -365,7 +366,8 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
   const int n = sh.count;
   const size_t out = (size_t)b * select;
   auto put = [&](int rank, double s, int32_t f) {
-    a.scores[out + rank] = (float)s;
+    // (a finite score past the largest float stays one: -inf goes with no candidate)
+    a.scores[out + rank] = s > -INFINITY ? fmaxf((float)s, -FLT_MAX) : -INFINITY;
     a.parents[out + rank] = s > -INFINITY ? f / vocab : -1;
     a.tokens[out + rank] = s > -INFINITY ? f % vocab : -1;
   };

@@ -77,3 +77,22 @@ def test_close_candidates_beside_dead_and_masked_beams():
     out = run(x, s, n, err=err)
     assert err.item() == pa.PA_DEVERR_LOGITS
     exact(out, x, s, n)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("V", [504, 40000])
+def test_scores_past_the_largest_float(dt, V):
+    """A beam score of the lowest float and logits masked with the type's lowest value add up past
+    it: such tokens stay candidates and their score is the lowest float; -inf goes with -1."""
+    low = torch.finfo(torch.float32).min
+    x = torch.full((40 * 3, V), torch.finfo(TDT[dt]).min, dtype=TDT[dt], device="cuda")
+    x[:, :2] = 1.0
+    s = torch.full((40, 3), low, device="cuda")
+    s[:, 1] = -math.inf
+    out = run(x, s, 9)
+    exact(out, x, s, 9, range(0, 40, 13))
+    assert bool((out[1] >= 0).all()) and bool((out[0] == low).all())
+    x[:, 2:] = -math.inf
+    scores, parents, _ = (t.cpu().numpy() for t in run(x, s, 9))
+    assert (parents == [0, 0, 2, 2, -1, -1, -1, -1, -1]).all()
+    assert np.array_equal(np.isinf(scores), parents < 0)
