@@ -270,7 +270,8 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
     for (int mask = 16; mask > 0; mask >>= 1) S += __shfl_xor_sync(0xffffffffu, S, mask);
     if (lane == 0) {
       double o = -INFINITY;
-      if (M > -INFINITY || S != S) o = M < INFINITY ? (double)beam - log(S) : NAN;
+      if (!(beam < INFINITY)) o = NAN;  // also where every token is masked
+      else if (M > -INFINITY || S != S) o = M < INFINITY ? (double)beam - log(S) : NAN;
       if (o != o || o == INFINITY) {  // a NaN or +inf among the logits, or as beam score
         report(a.dev_error, PA_DEVERR_LOGITS);
         o = -INFINITY;

@@ -96,3 +96,15 @@ def test_scores_past_the_largest_float(dt, V):
     scores, parents, _ = (t.cpu().numpy() for t in run(x, s, 9))
     assert (parents == [0, 0, 2, 2, -1, -1, -1, -1, -1]).all()
     assert np.array_equal(np.isinf(scores), parents < 0)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_bad_beam_score_is_reported_whatever_its_logits(bad):
+    x, s = make(2, 3, 700, "f32", 6)
+    x = x.clone()
+    x[1] = -math.inf                           # every token of the beam is masked
+    s[0, 1] = bad
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run(x, s, 5, err=err)
+    assert err.item() == pa.PA_DEVERR_LOGITS
+    check(out, x, s, 5)
