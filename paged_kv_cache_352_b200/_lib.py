@@ -1240,7 +1240,9 @@ class Scheduler:
         whose leading dimension covers the plan's counts; host_k/host_v are the
         pinned host pool (or None)."""
         torch = _torch()
-        code = _pool_dims(k_cache, v_cache)[4]
+        code = dtype_code(k_cache)      # pools of 16 or 8 bits may have any shape
+        if k_cache.dtype == torch.uint8 and k_cache.dim() == 4 and k_cache.shape[3] in (36, 68):
+            code = PA_INT4
         if (code == PA_FP8_E4M3) != getattr(self, "fp8", False) or (
                 code == PA_INT4) != getattr(self, "int4", False):
             raise PAError(PA_ERR_INVALID_ARG, "cache element type differs from the attached one")
