@@ -353,7 +353,7 @@ int pa_rope_and_cache_int4(void* q_out, const void* q, const void* key, const vo
 
 /* Host helper: fills cos_sin[num_positions][rotary_dim] (host memory) for the
  * frequencies theta^(-2i / rotary_dim), angles and functions in double
- * precision, rounded to float. */
+ * precision, rounded to float. theta from 1e-300 to 1e300. */
 int pa_rope_table(float* cos_sin, int num_positions, int rotary_dim, double theta);
 
 /* ---------------------------------------------------------------------------

@@ -1088,8 +1088,8 @@ int pa_rope_table(float* cos_sin, int num_positions, int rotary_dim, double thet
   if (rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16)
     return fail(PA_ERR_UNSUPPORTED, "rotary_dim %d: expected a multiple of 16 from 16 to 128",
                 rotary_dim);
-  if (!(theta > 0.0) || !(theta <= 1e300))
-    return fail(PA_ERR_INVALID_ARG, "theta must be positive and finite");
+  if (!(theta >= 1e-300) || !(theta <= 1e300))  // below: frequencies past the largest double
+    return fail(PA_ERR_INVALID_ARG, "theta must be positive and finite (1e-300 .. 1e300)");
   if (num_positions == 0) return PA_OK;
   if (!cos_sin) return fail(PA_ERR_INVALID_ARG, "null pointer argument");
   const int half = rotary_dim / 2;
