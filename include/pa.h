@@ -259,7 +259,7 @@ int pa_paged_decode_fp8(void* out, const void* q, const void* k_cache, const voi
  * type dtype (PA_F16 or PA_BF16). Workspace and order as pa_paged_decode. The
  * library's choice of partitions (partition_tokens 0) is pa_paged_decode_plan's,
  * but the unordered one also with a seq_order when num_seqs * num_kv_heads is
- * below 2048; few sequences of many partitions merge in a second launch. A pool
+ * below 1280; few sequences of many partitions merge in a second launch. A pool
  * must be below 2^38 bytes (PA_ERR_UNSUPPORTED).
  *
  * pa_read_slots_int4: the inverse of the write, for callers that attend to

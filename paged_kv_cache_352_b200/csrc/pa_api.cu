@@ -421,15 +421,16 @@ int paged_decode_impl(void* out, const void* q, const void* k_cache, const void*
           0xfffffffeLL)  // the kernel counts tile places in 64 bytes
     return fail(PA_ERR_UNSUPPORTED, "4-bit caches of 2^38 bytes or more are not supported");
   DecodeLayout lay;
-  // Over 4-bit caches a batch of up to 2 kSplitTargetUnits units keeps the 2048-token
-  // partitions of an unordered one: its launch is as long as its longest partition
-  // (128 sequences of 16-4096 tokens, 8 KV heads: 42.0 us with 4096-token partitions,
-  // 31.7 us with these, 35.3 us with 1024-token ones; 256 such sequences: 57.8, 62.3 and
-  // 74.3 us).
+  // Over 4-bit caches a batch of up to 5/4 kSplitTargetUnits units keeps the 2048-token
+  // partitions of an unordered one: its launch is as long as its longest partition, and
+  // above that partitions of 4096 cost fewer states and merges. us with 2048 / 4096 tokens
+  // (longest first, 32/8 heads, lognormal contexts up to 4096, 8192 and 16384 tokens):
+  // 384 units 33 / 38, 40 / 58, 82 / 70; 1024 units 37 / 45, 62 / 65, 117 / 105; 1280 units
+  // 44 / 45, 78 / 71, 146 / 132; 1536 units 51 / 50, 91 / 84, 174 / 156; 2048 units 66 / 62,
+  // 120 / 110, 230 / 208.
   const long long units = (long long)num_seqs * num_kv_heads;
-  const bool small_int4 = cache_dtype == PA_INT4 && units < kSplitTargetUnits;
   const bool ordered =
-      seq_order != nullptr && !(cache_dtype == PA_INT4 && units < 2 * kSplitTargetUnits);
+      seq_order != nullptr && !(cache_dtype == PA_INT4 && 4 * units < 5 * kSplitTargetUnits);
   if (int st = decode_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
                              partition_tokens, ordered, &lay))
     return st;
@@ -474,11 +475,14 @@ int paged_decode_impl(void* out, const void* q, const void* k_cache, const void*
   a.scale_log2 = scale * 1.4426950408889634f * k_scale;
   a.out_scale = v_scale;
   a.warp_parts = use_warp_parts(num_seqs, num_kv_heads, lay.part_blocks, lay.max_parts);
-  if (small_int4 && !a.warp_parts && forced_split() < 0 &&
-      units * lay.max_parts >= 2 * kSplitTargetUnits) {
+  if (cache_dtype == PA_INT4 && !a.warp_parts && forced_split() < 0 &&
+      units < kSplitTargetUnits / 8 && units * lay.max_parts >= 2 * kSplitTargetUnits) {
     // Few sequences of many partitions: a quarter of a partition per warp and a merge
-    // launch instead of a merge by each sequence's last CTA (140.0 -> 134.3 us on
-    // that batch; 256 sequences of 16-4096 tokens lose by it, 75.6 -> 138.0 us).
+    // launch instead of a merge by each sequence's last CTA. us in this form / merged by the
+    // last CTA, 8 query heads per KV head: 64 units of 32k-131k tokens 132 / 136, of 131k
+    // 218 / 227, of 65k 118 / 124; 96 units 186 / 190; 4 heads, 64 units 132 / 134. 16 and 32
+    // units are alike; 128 units of 16k-65k 161 / 159, 256 units 343 / 336, and of shorter
+    // contexts the form loses up to a third (512 units of 1k-8k 95 / 76).
     // States are one row per partition, as laid out.
     a.warp_parts = 2;
     a.part_blocks = (lay.part_blocks + 3) / 4;

@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 # (sequences, KV heads, longest context, partition): the second launch over CTAs' partitions takes
-# fewer than 1024 (sequence, KV head) pairs that give 2048 partitions and more
+# fewer than 128 (sequence, KV head) pairs that give 2048 partitions and more
 QUARTERED = [(8, 4, 1040, 16), (8, 4, 2100, 32), (8, 4, 3120, 48), (8, 4, 7200, 112),
              (4, 8, 5200, 80)]
 
@@ -109,3 +109,16 @@ def test_forced_merge_by_the_last_cta():
     r = subprocess.run([sys.executable, "-c", FORCED], capture_output=True, text=True, env=env,
                        cwd=ROOT, timeout=300)
     assert r.returncode == 0 and "alike" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("seqs,hkv", [(40, 8), (159, 8), (160, 8), (161, 8), (320, 4), (256, 8)])
+def test_sizes_around_the_partition_rule(seqs, hkv):
+    """Longest first, partitions of the library's choice, on both sides of 1280 (sequence, KV head)
+    pairs: workspaces of the plan's size hold, and the rows are the oracle's."""
+    ctx = np.random.default_rng(seqs).integers(1, 60, seqs)
+    ctx[[0, seqs // 2, seqs - 1]] = 5000, 4097, 2049
+    b = Batch(ctx, 2 * hkv, hkv, 64, "f16", seqs)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = b.run(0, order=True, err=err)
+    assert err.item() == 0
+    b.check(out, rows=[0, 1, seqs // 2, seqs - 1])
