@@ -366,10 +366,10 @@ int pa_rope_table(float* cos_sin, int num_positions, int rotary_dim, double thet
  * x the logits of row b * num_beams + k, the num_select largest scores of all
  * (k, v), best first, ties to the smaller k * vocab + v: their scores, beams and
  * tokens. Scores are ranked in double precision and rounded to float; their
- * logarithms come from fp32 sums of exponentials, within 8e-6 (1e-6 and less in
- * practice). Candidates of different beams closer than 2^-18 are ordered by sums
- * in double precision, so that beams that are copies tie and only candidates of
- * sums off by more than 2^-19 could change places with others'. A score
+ * logarithms come from fp32 sums of exponentials, within 8e-6 (5.2e-7 at most
+ * where measured). Candidates of different beams closer than 2^-19 are ordered by
+ * sums in double precision, so that beams that are copies tie and only candidates
+ * of sums off by more than 2^-20 (9.5e-7) could change places with others'. A score
  * of -inf is no candidate: a beam score of -inf (an ended beam, or all but one
  * before the first step) or a logit of -inf (a masked token) takes it out. A beam
  * with a NaN or +inf among its logits, or as its score, gives no candidates
