@@ -203,7 +203,7 @@ __device__ __forceinline__ double exact_share(const T* x, int vocab, double larg
 // order that depends on the row and the CTA's threads alone. partial: [kThreads / 32] of
 // shared memory.
 template <int kThreads>
-__device__ __noinline__ double exact_sum(const BeamArgs& a, size_t row, float largest,
+__device__ __forceinline__ double exact_sum(const BeamArgs& a, size_t row, float largest,
                                          double* partial) {
   const int64_t first = (int64_t)row * a.row_stride;
   double S;
@@ -223,6 +223,44 @@ __device__ __noinline__ double exact_sum(const BeamArgs& a, size_t row, float la
   S = 0.0;
   for (int w = 0; w < kThreads / 32; ++w) S += partial[w];
   return S;
+}
+
+// Result `rank` of sequence b.
+__device__ __forceinline__ void put_result(const BeamArgs& a, int b, int rank, double s,
+                                           int32_t f) {
+  const size_t out = (size_t)b * a.select + rank;
+  // (a finite score past the largest float stays one: -inf goes with no candidate)
+  a.scores[out] = s > -INFINITY ? fmaxf((float)s, -FLT_MAX) : -INFINITY;
+  a.parents[out] = s > -INFINITY ? f / a.vocab : -1;
+  a.tokens[out] = s > -INFINITY ? f % a.vocab : -1;
+}
+
+// Takes the sums of the rows in sh.near again and, unless there were too many (n >
+// kMergeCap), ranks the n collected candidates by them. A function of its own, so that
+// the registers and the code of calls that need it are not others'.
+template <int kThreads>
+__device__ __noinline__ void rank_again(const BeamArgs& a, int b, int n,
+                                        MergeShared<kThreads / 32>& sh, double* cs, int32_t* cf) {
+  const unsigned long long near = sh.near;
+  for (int k = 0; k < a.num_beams; ++k) {
+    if (!(near >> k & 1)) continue;
+    const size_t row = (size_t)b * a.num_beams + k;
+    const double S = exact_sum<kThreads>(a, row, sh.largest[k], sh.warp_best);
+    if (threadIdx.x == 0) sh.offset[k] = (double)a.beam_scores[row] - log(S);
+  }
+  __syncthreads();
+  if (n > kMergeCap) return;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int k = cf[i] / a.vocab;
+    const float x = any_logit(a, (size_t)b * a.num_beams + k, cf[i] % a.vocab);
+    cs[i] = ((double)x - (double)sh.largest[k]) + sh.offset[k];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += before(cs[j], cf[j], cs[i], cf[i]);
+    if (rank < a.select) put_result(a, b, rank, cs[i], cf[i]);
+  }
 }
 
 // Sequence b by one CTA: its rows' logsumexp, then its best candidates. cs, cf: shared
@@ -286,15 +324,12 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
     sh.near = 0;
   }
   __syncthreads();
-  auto score = [&](float x, int k) {
-    return ((double)x - (double)sh.largest[k]) + sh.offset[k];
-  };
   auto score_key = [&](int i, uint64_t key, double& s, int32_t& f) {
     const int k = i / per_beam;
     s = -INFINITY;
     f = INT32_MAX;
     if (key != 0 && sh.offset[k] > -INFINITY) {
-      s = score(from_orderable((uint32_t)(key >> 32)), k);
+      s = ((double)from_orderable((uint32_t)(key >> 32)) - (double)sh.largest[k]) + sh.offset[k];
       f = k * vocab + (int32_t)~(uint32_t)key;  // below 2^30
     }
   };
@@ -366,35 +401,27 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
   }
   __syncthreads();
   const int n = sh.count;
-  const size_t out = (size_t)b * select;
-  auto put = [&](int rank, double s, int32_t f) {
-    // (a finite score past the largest float stays one: -inf goes with no candidate)
-    a.scores[out + rank] = s > -INFINITY ? fmaxf((float)s, -FLT_MAX) : -INFINITY;
-    a.parents[out + rank] = s > -INFINITY ? f / vocab : -1;
-    a.tokens[out + rank] = s > -INFINITY ? f % vocab : -1;
+  auto mark = [&](int k, int l) {
+    if (k != l) atomicOr(&sh.near, 1ull << k | 1ull << l);
   };
-  auto rank_all = [&](auto&& use) {  // of every candidate that was collected
+  if (n <= kMergeCap) {
     for (int i = threadIdx.x; i < n; i += kMergeThreads) {
       const double s = cs[i];
       const int32_t f = cf[i];
       int rank = 0;
       for (int j = 0; j < n; ++j) rank += before(cs[j], cf[j], s, f);
-      if (rank < select) use(rank, s, f);
+      if (rank < select) {
+        put_result(a, b, rank, s, f);
+        sh.top[rank] = s;
+        sh.top_index[rank] = f;
+      }
     }
-  };
-  const int places = min(n, select);
-  if (n <= kMergeCap) {
-    rank_all([&](int rank, double s, int32_t f) {
-      sh.top[rank] = s;
-      sh.top_index[rank] = f;
-    });
+    for (int i = n + threadIdx.x; i < select; i += kMergeThreads)
+      put_result(a, b, i, -INFINITY, 0);
     __syncthreads();
     // Beams whose candidates lie closer than their sums' rounding: neighbours in the order,
     // and what might still come to the last place.
-    auto mark = [&](int k, int l) {
-      if (k != l) atomicOr(&sh.near, 1ull << k | 1ull << l);
-    };
-    for (int i = threadIdx.x; i + 1 < places; i += kMergeThreads)
+    for (int i = threadIdx.x; i + 1 < min(n, select); i += kMergeThreads)
       if (sh.top[i] - sh.top[i + 1] <= kNear)
         mark(sh.top_index[i] / vocab, sh.top_index[i + 1] / vocab);
     if (n > select) {
@@ -409,32 +436,9 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
   }
   __syncthreads();
   const unsigned long long near = sh.near;
-  if (near & (near - 1)) {  // (alone, a beam's order is its logits')
-    for (int k = 0; k < beams; ++k) {
-      if (!(near >> k & 1)) continue;
-      const size_t row = (size_t)b * beams + k;
-      const double S = exact_sum<kMergeThreads>(a, row, sh.largest[k], sh.warp_best);
-      if (threadIdx.x == 0) sh.offset[k] = (double)a.beam_scores[row] - log(S);
-    }
-    __syncthreads();
-    if (n <= kMergeCap) {
-      for (int i = threadIdx.x; i < n; i += kMergeThreads) {
-        const int k = cf[i] / vocab;
-        cs[i] = score(any_logit(a, (size_t)b * beams + k, cf[i] % vocab), k);
-      }
-      __syncthreads();
-      rank_all([&](int rank, double s, int32_t f) {
-        sh.top[rank] = s;
-        sh.top_index[rank] = f;
-      });
-      __syncthreads();
-    }
-  }
-  if (n <= kMergeCap) {
-    for (int i = threadIdx.x; i < select; i += kMergeThreads)
-      put(i, i < places ? sh.top[i] : -INFINITY, i < places ? sh.top_index[i] : 0);
-    return;
-  }
+  // (one alone: a beam's order is its logits')
+  if (near & (near - 1)) rank_again<kMergeThreads>(a, b, n, sh, cs, cf);
+  if (n <= kMergeCap) return;
   // more equal candidates than the buffer holds: one at a time
   double ls = INFINITY;
   int32_t lf = -1;
@@ -470,7 +474,7 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
         s = sh.best_score[w];
         f = sh.best_index[w];
       }
-    if (threadIdx.x == 0) put(r, s, f);
+    if (threadIdx.x == 0) put_result(a, b, r, s, f);
     ls = s;
     lf = f;
   }
