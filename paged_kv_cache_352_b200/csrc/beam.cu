@@ -40,6 +40,7 @@
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
+#include <stddef.h>
 #include <string.h>
 
 #include <type_traits>
@@ -161,6 +162,7 @@ struct MergeShared {
   // sum of exponentials relative to the row's largest logit, -inf for a dead beam
   __align__(16) double offset[PA_BEAM_MAX];
   __align__(16) float largest[PA_BEAM_MAX];
+  __align__(16) float beam[PA_BEAM_MAX];  // beam scores
   __align__(16) double group_max[kGroups];
   __align__(16) double warp_best[kWarps];
   __align__(16) double best_score[kWarps];
@@ -246,7 +248,7 @@ __device__ __noinline__ void rank_again(const BeamArgs& a, int b, int n,
     if (!(near >> k & 1)) continue;
     const size_t row = (size_t)b * a.num_beams + k;
     const double S = exact_sum<kThreads>(a, row, sh.largest[k], sh.warp_best);
-    if (threadIdx.x == 0) sh.offset[k] = (double)a.beam_scores[row] - log(S);
+    if (threadIdx.x == 0) sh.offset[k] = (double)sh.beam[k] - log(S);
   }
   __syncthreads();
   if (n > kMergeCap) return;
@@ -317,6 +319,7 @@ __device__ __forceinline__ void merge_sequence(const BeamArgs& a, const Work& wo
       }
       sh.offset[k] = o;
       sh.largest[k] = M;
+      sh.beam[k] = beam;
     }
   }
   if (threadIdx.x == 0) {
@@ -518,6 +521,9 @@ __global__ void __launch_bounds__(kBeamThreads, 4)
     int count, last_piece;
   };
   __shared__ Shared sh;
+  // every group has four threads, and its maximum is read 16 bytes at a time
+  static_assert(kBeamThreads == 4 * kGroups, "groups of four neighbouring lanes");
+  static_assert(offsetof(Shared, group_max) % 16 == 0 && alignof(Shared) % 16 == 0, "alignment");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int vocab = a.vocab, select = a.select;
   const int total = a.num_seqs * a.num_beams * chunks;
