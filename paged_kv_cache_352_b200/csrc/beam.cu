@@ -10,15 +10,17 @@
 // its N largest logits in the workspace; then one CTA per sequence adds up the rows'
 // sums and ranks K x pieces x N candidates. For little work a piece is 8 or 16 logits a
 // thread and the CTA that finishes the sequence's last piece merges it (4 beams of 32000
-// logits: 6.7 us; a second launch cost 2.6 us more). For much work 4 CTAs an SM each walk
+// logits: 8 us; a second launch cost 2.6 us more). For much work 4 CTAs an SM each walk
 // an equal share of the rows laid end to end, as pieces of up to 16 chunks, and a second
 // launch merges: its launch is cheaper than every CTA's wait for the release of its
-// results. 64 x 8 beams of 131072 bf16 logits take 37.3 us, 31 of them reading (20.8 at
-// the copy rate); 41.1 us with a CTA and a piece per 16384 logits, 41.3 and 42.5 us with
-// shares of at most 8 and 4 chunks, 40.9 us with chunks copied two ahead through shared
-// memory (fewer waits, more instructions), 43.2 us with 3 CTAs an SM. What is left is
-// spread over the exponentials (half of their pipe's rate), issue (45 %), the ends of the
-// pieces and SMs that finish 10 % apart.
+// results. 64 x 8 beams of 131072 bf16 logits take 38 us, 31 of them reading (20.8 at
+// the copy rate). Other forms, in one run with this one at 37.3 us: 41.1 with a CTA and a
+// piece per 16384 logits, 41.3 and 42.5 with shares of at most 8 and 4 chunks, 40.9 with
+// chunks copied two ahead through shared memory (fewer waits, more instructions), 43.2 with
+// 3 CTAs an SM. No pipe is above half of its rate (exponentials 50 %, issue 45 %, DRAM
+// 49 %); the largest stall is the wait for loads: a piece's last step loads the chunk that it
+// has just taken once more, nothing is in flight while a piece is ranked, which most shares
+// do twice, and SMs finish 10 % apart.
 //
 // The N largest of a piece without sorting it: the N-th largest of the maxima of
 // kGroups groups of threads bounds the N-th largest element from below, so the few

@@ -11,8 +11,11 @@
 //
 // What bounds it. A (block, KV head) takes 16 (d + 8) bytes, of which an SM's share
 // of the memory stream brings one every 95 cycles (d = 128, 1.9 GHz); its four
-// schedulers then have 380 issue slots a tile. Half of them go to turning
-// codes into operands and multiplying, so the loop is built for few instructions:
+// schedulers then have 380 issue slots a tile. The loop takes about 215 instructions a
+// tile, 88 of them turning codes into operands and 17 products, and a warp some 1500 more
+// around it (ncu: issue 63 %, ALU 54 %, DRAM 56 %; the largest stalls are fixed latencies
+// and warps not selected: no pipe is full, and 16 warps an SM leave chains uncovered).
+// It is built for few instructions:
 //   - every product runs on mma.sync, also for one query head per KV head (the
 //     padding columns cost tensor time that is not short: 8 cycles per instruction,
 //     17 a tile). The contraction has G columns of work, far too few for tcgen05;
@@ -35,10 +38,11 @@
 //   - a step takes two blocks: one vote, one wait for 32 tokens, and two
 //     independent chains of products.
 //
-// Measured: 64 sequences of 128-2048 tokens, 32 heads, d = 128, f16 (337 MB): 66 us,
-// 5.1 TB/s; the other caches' loop over these tiles took 105.5 us, the same loads without
-// arithmetic take 53.9 us, a copy of the bytes 52.1 us. 8 sequences of 32768-131072 tokens,
-// 64 query and 8 KV heads, bf16: 131 us (loads alone 114).
+// Measured: 64 sequences of 128-2048 tokens, 32 heads, d = 128, f16 (337 MB): 69 us,
+// 4.9 TB/s, in short bursts, 77 us in a loop of seconds (power limit, lower clock); the other
+// caches' loop over these tiles took 105.5 us, the same loads without arithmetic take
+// 53.9 us, a copy of the bytes 52.1 us. 8 sequences of 32768-131072 tokens, 64 query and 8
+// KV heads, bf16: 139 and 160 us (loads alone 114).
 //
 // S = K Q^T. Lane 4g + c holds k-slots 2c, 2c+1, 2c+8, 2c+9 of A (rows g, g + 8)
 // and of B (column g). It takes dimensions 8W c .. 8W c + 8W - 1 (W = d/32 words a
@@ -49,7 +53,8 @@
 // O^T = V^T P^T. A value word holds four dimensions of tokens 2p, 2p+1: word q of
 // pair c gives a0 (dimension 4Wg + 4q) and a1 (+1), of pair c + 4 a2 and a3;
 // shifted, dimensions +2 and +3 for the next m-tile. The result's columns are
-// heads 2c, 2c + 1 again. One more product with ones for V gives sum w.
+// heads 2c, 2c + 1 again. One more product with ones for V gives sum w, from which the
+// others start.
 //
 // Precision. Products are exact, sums are fp32. The matrix instruction, though, cuts its
 // addends (towards zero) at about 2^-24 of the largest, and takes a subnormal code's size from

@@ -19,9 +19,12 @@
 // the chains slot -> place and position -> angles -> row: the first rows are loaded before
 // them, and further rows while the ones before are turned.
 //
-// Measured: 16384 tokens of 32 + 8 heads, d = 128, 16-bit: 67.7 us, 6.1 TB/s (94 % of a
-// copy); 4096 tokens 21.1 us, into E4M3 24.2 us, into 4 bits 23.7 us (the quantization's
-// instructions: 40 % of issue), read back 6.2 us.
+// Measured (inputs that rotate over four sets): 16384 tokens of 32 + 8 heads, d = 128, 16-bit:
+// 67.6 us, 6.1 TB/s (94 % of a copy), into E4M3 76, into 4 bits 76; 4096 tokens 21.6 us
+// (15.9 at the copy rate), into E4M3 25.1 (14.6; every element is divided by the scale,
+// IEEE, as the format's codes are defined), into 4 bits 24.6 (14.0), written in 4 bits without
+// queries 10.7 (3.3), read back 6.7 (3.3). 4096 tokens are 1536 CTAs, 1.7 to 2.1 times what is
+// resident at once: every wave starts with the chain of lookups, and the last is part filled.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -36,9 +39,10 @@ namespace {
 constexpr int kRopeThreads = 128;
 
 // Rows of each token that a lane group holds at once (as many again are on their way), and
-// CTAs per SM (96 or 80 registers). 4096 tokens of 32 + 8 heads, five and six CTAs: E4M3 24.9
-// and 23.7 us, 4 bits 23.7 and 23.2 us; 16-bit, 16384 tokens: 69.5 and 71.0 us. Four rows
-// loaded at once and none ahead took 27.4, 25.1 and 69.1 us.
+// CTAs per SM (96 or 80 registers). 4096 tokens of 32 + 8 heads, five and six CTAs, in one run
+// (its figures are 5 % below those above): E4M3 24.9 and 23.7 us, 4 bits 23.7 and 23.2 us;
+// 16-bit, 16384 tokens: 69.5 and 71.0 us. Four rows loaded at once and none ahead took 27.4,
+// 25.1 and 69.1 us.
 template <typename C>
 struct RopeShape {
   static constexpr int kUnroll = 2, kCtasPerSm = 5;
