@@ -42,7 +42,7 @@
 // 4.9 TB/s, in short bursts, 77 us in a loop of seconds (power limit, lower clock); the other
 // caches' loop over these tiles took 105.5 us, the same loads without arithmetic take
 // 53.9 us, a copy of the bytes 52.1 us. 8 sequences of 32768-131072 tokens, 64 query and 8
-// KV heads, bf16: 139 and 160 us (loads alone 114).
+// KV heads, bf16: 160 and 182 us (loads alone 114).
 //
 // S = K Q^T. Lane 4g + c holds k-slots 2c, 2c+1, 2c+8, 2c+9 of A (rows g, g + 8)
 // and of B (column g). It takes dimensions 8W c .. 8W c + 8W - 1 (W = d/32 words a
@@ -64,7 +64,7 @@
 // additions, rounded to nearest. With running sums as the accumulator and codes at 2^-24 and
 // 2^-20, half outputs over 131072 tokens of normal scores were off by 2.4e-4 of their norm
 // beside their rounding's 2.1e-4; now by 7e-6 (scores twice as wide: 5.7e-4, 7e-5). It costs
-// 3.5 % (one head per KV head), 3.5 % (4) and 4 % (8). q is brought below 2^15 by a
+// 3.5 to 4 %. q is brought below 2^15 by a
 // power of two (exact in half unless 2^28 below the row's largest element, or 2^24 at the
 // dimensions of high nibbles, whose operand is q / 16: 2^-35 of that element is lost). The
 // weights w are rounded to half precision in units that put the largest at 2^6 to 2^7 when
@@ -74,11 +74,10 @@
 // 7.5 sum w is taken over the rounded weights, so that their errors multiply the
 // centred codes. What the rounding leaves of w joins the products too, rounded to half
 // again (2^-22 of w in all): with at most 4 query heads per KV head heads repeat in
-// columns 4-7, whose lanes feed it, with 8 it is a second product for half outputs.
-// For bf16 outputs of 8 heads w stays at its 2^-12, a sixteenth of half the output's step:
-// the second product took 8 long sequences from 154 to 173 us and brought the outputs'
-// relative difference from 32-bit sums from 1.0e-3 to 0.8e-3; with 4 heads,
-// where it costs 3 %, from 8e-4 to 2e-4.
+// columns 4-7, whose lanes feed it; with 8 it is a second product with sums of its own (in
+// one chain with the weights' it would be cut at their size). Without it bf16 outputs over
+// these contexts differ from 32-bit sums by 8e-4 to 1e-3 of their norm, with it by 1e-4; it
+// costs 3 % (4 heads) and 14 % (8; 160 -> 182 us for the long contexts, 138 -> 160 in a burst).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -86,7 +85,6 @@
 #include <string.h>
 
 #include <atomic>
-#include <type_traits>
 
 #include "decode_common.cuh"
 #include "decode_merge.cuh"
@@ -180,7 +178,6 @@ struct Int4State {
   static constexpr int kCodeBytes = kBlockSize * D / 2;
   static constexpr int kTileBytes = int4_tile_bytes(D);
   static constexpr bool kRepeat = G <= 4;  // columns 4-7 repeat heads 0-3
-  static constexpr bool kSecond = G == 8 && std::is_same<T, __half>::value;  // residuals' own
   static constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;
 
   int g, c, lane;
@@ -396,14 +393,14 @@ struct Int4State {
         memcpy(&lo[b][i], &rl, 4);
         pb[b][i] = r.h[b][i];
         if constexpr (kRepeat) pb[b][i] = c < 2 ? pb[b][i] : lo[b][i];
-        else if constexpr (kSecond) lo[b][i] = transpose8(lo[b][i]);
+        else lo[b][i] = transpose8(lo[b][i]);
         pb[b][i] = transpose8(pb[b][i]);
       }
     constexpr uint32_t kOnes = 0x3c003c00u;
     float sw[4] = {0.f, 0.f, 0.f, 0.f};
     mma_16816(sw, kOnes, kOnes, kOnes, kOnes, pb[0][0], pb[0][1]);
     mma_16816(sw, kOnes, kOnes, kOnes, kOnes, pb[1][0], pb[1][1]);
-    if constexpr (kSecond) {
+    if constexpr (!kRepeat) {
       float sl[4] = {0.f, 0.f, 0.f, 0.f};
       mma_16816(sl, kOnes, kOnes, kOnes, kOnes, lo[0][0], lo[0][1]);
       mma_16816(sl, kOnes, kOnes, kOnes, kOnes, lo[1][0], lo[1][1]);
@@ -431,10 +428,15 @@ struct Int4State {
         a[b][0] = x & 4 * kLo, a[b][1] = x & 4 * kHi, a[b][2] = y & 4 * kLo, a[b][3] = y & 4 * kHi;
       }
       mma_16816_from(d, start, a[0][0], a[0][1], a[0][2], a[0][3], pb[0][0], pb[0][1]);
-      mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], pb[1][0], pb[1][1]);
-      if constexpr (kSecond) {  // behind the weights, whose sum is near 0 by now
-        mma_16816(d, a[0][0], a[0][1], a[0][2], a[0][3], lo[0][0], lo[0][1]);
-        mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], lo[1][0], lo[1][1]);
+      if constexpr (!kRepeat) {  // two chains: the residuals' own, joined below
+        float r[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_16816(r, a[0][0], a[0][1], a[0][2], a[0][3], lo[0][0], lo[0][1]);
+        mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], pb[1][0], pb[1][1]);
+        mma_16816(r, a[1][0], a[1][1], a[1][2], a[1][3], lo[1][0], lo[1][1]);
+        fadd2(d[0], d[1], r[0], r[1]);
+        fadd2(d[2], d[3], r[2], r[3]);
+      } else {
+        mma_16816(d, a[1][0], a[1][1], a[1][2], a[1][3], pb[1][0], pb[1][1]);
       }
       fadd2(o[t][0], o[t][1], d[0], d[1]);
       fadd2(o[t][2], o[t][3], d[2], d[3]);

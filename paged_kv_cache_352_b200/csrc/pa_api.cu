@@ -479,10 +479,11 @@ int paged_decode_impl(void* out, const void* q, const void* k_cache, const void*
       units < kSplitTargetUnits / 8 && units * lay.max_parts >= 2 * kSplitTargetUnits) {
     // Few sequences of many partitions: a quarter of a partition per warp and a merge
     // launch instead of a merge by each sequence's last CTA. us in this form / merged by the
-    // last CTA, 8 query heads per KV head: 64 units of 32k-131k tokens 132 / 136, of 131k
-    // 218 / 227, of 65k 118 / 124; 96 units 186 / 190; 4 heads, 64 units 132 / 134. 16 and 32
-    // units are alike; 128 units of 16k-65k 161 / 159, 256 units 343 / 336, and of shorter
-    // contexts the form loses up to a third (512 units of 1k-8k 95 / 76).
+    // last CTA, 8 query heads per KV head: 64 units of 32k-131k tokens 152 / 156, of 131k
+    // 254 / 264, of 65k 137 / 142; 96 units 215 / 218; 4 heads, 64 units 132 / 134. 16 and 32
+    // units are alike; 128 units of 16k-65k 161 / 159, 256 units 343 / 336 (before the
+    // residuals' second product), and of shorter contexts the form loses up to a third (512
+    // units of 1k-8k 95 / 76).
     // States are one row per partition, as laid out.
     a.warp_parts = 2;
     a.part_blocks = (lay.part_blocks + 3) / 4;

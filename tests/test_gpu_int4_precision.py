@@ -5,8 +5,7 @@ With p_t the softmax weights, s_t and mid_t the value rows' parameters, P = sum 
   scores   as in test_gpu_int4: a weight is off by at most e_p = 2 dx + 2^-20 of itself,
            dx = X 142 2^-23, so an output by 2 e_p sum p_t |v_t| / P
   weights  w_t = p_t s_t is kept to 2^-20 of itself and to 2^-30 of the largest one
-           (a half and the half of what that rounds off; for bf16 outputs of 8 query heads per
-           KV head the first alone, 2^-11), and acts on centred codes of at most 7.5
+           (a half and the half of what that rounds off), and acts on centred codes of at most 7.5
   sums     of a step (two blocks) the matrix instruction cuts its addends at 2^-23 of the largest,
            a code's operand counting as 2^9 of it, so at 2^-14 of the step's largest w: the running
            sum in each of at most 8 products, and of the weights' products those of an eighth of
@@ -70,8 +69,7 @@ def bound(b, s, h):
     ref = p @ v / P
     w = p * np.abs(vp[:, 0])
     centred = p @ np.abs(v - vp[:, 1:]) / P
-    e_w = 2.0 ** -11 if b.dt == "bf16" and b.hq == 8 * b.hkv else 2.0 ** -20
-    lost = (2 * e_p * (p @ np.abs(v)) / P + 7.5 * (e_w * w.sum() + n * 2.0 ** -30 * w.max()) / P
+    lost = (2 * e_p * (p @ np.abs(v)) / P + 7.5 * (2.0 ** -20 * w.sum() + n * 2.0 ** -30 * w.max()) / P
             + (cut_in_steps(w) + 255 * 2.0 ** -23 * w.sum()) / P
             + (n / 128 + 64) * 2.0 ** -24 * centred)
     return ref, lost + half_step(np.abs(ref) + lost, b.dt) + 2.0 ** -25
